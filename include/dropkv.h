@@ -40,7 +40,7 @@
 extern "C" {
 #endif
 
-#define DROPKV_ABI_VERSION 2
+#define DROPKV_ABI_VERSION 3
 
 #if defined(__GNUC__)
 #define DROPKV_API __attribute__((visibility("default")))
@@ -61,7 +61,9 @@ typedef enum dropkv_status {
 typedef enum dropkv_dtype {
   DROPKV_BF16 = 0,  /* q, k, v stored as bfloat16; arithmetic in fp32 (tensor-core
                        operands bf16 with fp32 accumulation)                          */
-  DROPKV_F32 = 1    /* q, k, v stored as float32; arithmetic in fp64 (CUDA cores)      */
+  DROPKV_F32 = 1,   /* q, k, v stored as float32; arithmetic in fp64 (CUDA cores)      */
+  DROPKV_E4M3 = 2   /* cache pages only: 8-bit floats (4 exponent, 3 mantissa bits)
+                       with one power-of-two scale per row                            */
 } dropkv_dtype;
 
 /* Which kernels compute the scores (dropkv_options.path). */
@@ -256,6 +258,120 @@ DROPKV_API dropkv_status dropkv_scores_select(const dropkv_shape* shape, const v
                                               void* workspace, size_t workspace_bytes,
                                               void* stream, int32_t* status_dev,
                                               const dropkv_options* options);
+
+/* ---- paged K/V cache -----------------------------------------------------------
+ *
+ * What an eviction keeps, and the tokens that come after it, live in pages: a
+ * sequence's slot j is row j % page_size of page page_table[b][j / page_size].
+ * Three entry points work on the pages: dropkv_cache_write (dense rows to
+ * slots, as they are or quantised), dropkv_cache_read (slots to dense rows) and
+ * dropkv_cache_attention (a chunk of new tokens over the slots).
+ *
+ * Differences from the conventions above: sequence lengths, starts, counts and
+ * the page table are DEVICE arrays (they change from step to step, also under a
+ * replayed graph), and the dense tensors may be strided.  Values in device
+ * arrays cannot be checked on the host; the kernels check them: a page outside
+ * [0, n_pages), a slot outside [0, max_pages * page_size), a row outside its
+ * tensor, and a length or count outside its range touch no memory, count as
+ * absent (lengths and counts are clamped), and raise DROPKV_ERR_ARG in
+ * *status_dev.  status_dev (device int32) may be NULL: then nothing is reported.
+ * All three are asynchronous on `stream`, allocate nothing and can be captured
+ * into a graph.  A graph's replays must not overlap other calls that use its
+ * workspace.
+ *
+ * E4M3 pages: a row x of d values is stored as byte = e + 127 and the values
+ * x * 2^-e rounded to nearest even, with e >= -127 the least integer for which
+ * max |x| <= 448 * 2^e (a row of zeros: byte 0).  A power of two costs an 8-bit
+ * float no precision, makes scaling exact in both directions, and makes the
+ * stored bits independent of the arithmetic.  A row that holds an infinity or a
+ * NaN is stored as byte 255 and reads back as NaN.
+ */
+typedef struct dropkv_cache {
+  int32_t B;            /* sequences (rows of the page table), >= 1                 */
+  int32_t Hkv;          /* KV heads, >= 1                                           */
+  int32_t d;            /* head dimension, 1..256                                   */
+  int32_t n_pages;      /* pages in the pools, >= 1                                 */
+  int32_t page_size;    /* slots of a page, 1..1024                                 */
+  int32_t max_pages;    /* pages a sequence can have (row stride of the page table) */
+  int32_t dtype;        /* dropkv_dtype of the pages                                */
+  int32_t reserved;     /* 0                                                        */
+  void* k_pages;        /* device [n_pages, Hkv, page_size, d]                      */
+  void* v_pages;
+  uint8_t* k_scale;     /* device [n_pages, Hkv, page_size] for E4M3, else NULL     */
+  uint8_t* v_scale;
+  const int32_t* page_table;  /* device int32 [B, max_pages]                        */
+} dropkv_cache;
+
+/* The dense side of a write or a read.  Strides are in elements, for
+ * (sequence, head, row); the last index (d) is contiguous. */
+typedef struct dropkv_cache_rows {
+  void* k;              /* device [B, Hkv, n, d], strided; a write only reads it    */
+  void* v;
+  int64_t k_stride[3];
+  int64_t v_stride[3];
+  int32_t dtype;        /* DROPKV_BF16 or DROPKV_F32                                */
+  int32_t n;            /* rows of the dense tensors per (sequence, head)           */
+  int32_t m;            /* rows moved at most per (sequence, head), >= 1; without a
+                           list, and on a read, m <= n                              */
+  int32_t reserved;     /* 0                                                        */
+  const int32_t* rows;  /* device int32 [B, Hkv, m] or NULL: the list (a keep_idx of
+                           dropkv_select is one); an entry of -1 is skipped         */
+  const int32_t* start; /* device int32 [B], or NULL for 0                          */
+  const int32_t* counts;/* device int32 [B]: rows moved, 0..m; NULL for m           */
+} dropkv_cache_rows;
+
+/* Slot start[b] + i of every head of sequence b receives dense row i (row
+ * rows[b][h][i] with a list), for i < counts[b].  Other slots stay as they are.
+ * Two rows for one slot (pages that occur twice) leave either of them. */
+DROPKV_API dropkv_status dropkv_cache_write(const dropkv_cache* cache,
+                                            const dropkv_cache_rows* rows, int32_t* status_dev,
+                                            void* stream);
+
+/* Dense row i receives slot start[b] + i (slot start[b] + rows[b][h][i] with a
+ * list), for i < counts[b], rounded to the dense type.  Other dense rows stay
+ * as they are. */
+DROPKV_API dropkv_status dropkv_cache_read(const dropkv_cache* cache,
+                                           const dropkv_cache_rows* rows, int32_t* status_dev,
+                                           void* stream);
+
+/* A chunk of up to T new tokens per sequence over its slots.  With L =
+ * lengths[b] slots, the chunk's own tokens (written beforehand) being the last
+ * n = q_lengths[b] of them, row t < n sits at position L - n + t and sees the
+ * slots 0..L - n + t (all L without `causal`):
+ *   out = softmax(scale q . k_j) v_j,   lse = log sum_j exp(scale q . k_j).
+ * A row that sees nothing gets out = 0 and lse = -inf.  What a row does not see
+ * has no influence on it, whatever it holds (NaN included).  Rows t >= n of out
+ * and lse stay as they are.  Query head hq uses KV head hq / (Hq / Hkv). */
+typedef struct dropkv_cache_attn {
+  const void* q;        /* device [B, Hq, T, d], strided (last index contiguous)    */
+  void* out;            /* device [B, Hq, T, d], strided                            */
+  float* lse;           /* device fp32 [B, Hq, T] dense, or NULL                    */
+  int64_t q_stride[3];  /* elements, for (sequence, head, token)                    */
+  int64_t out_stride[3];
+  int32_t dtype;        /* DROPKV_BF16 or DROPKV_F32, of q and out                  */
+  int32_t Hq;           /* a multiple of the cache's Hkv                            */
+  int32_t T;            /* >= 1                                                     */
+  int32_t causal;       /* 0 or 1                                                   */
+  float scale;          /* > 0, or 0 for 1/sqrt(d)                                  */
+  int32_t path;         /* dropkv_path: AUTO, SIMT (fp32 CUDA cores, any shape) or
+                           TENSOR (bf16 q; bf16 or E4M3 pages; d 64 or 128; q, out
+                           and their strides multiples of 16 bytes)                 */
+  const int32_t* lengths;   /* device int32 [B], 0..max_pages * page_size           */
+  const int32_t* q_lengths; /* device int32 [B], 0..T, or NULL for T                */
+} dropkv_cache_attn;
+
+/* Bytes of workspace dropkv_cache_attention needs for these sizes and this path
+ * (no pointer of the two structs is read).  0 if they are invalid. */
+DROPKV_API size_t dropkv_cache_attention_workspace_bytes(const dropkv_cache* cache,
+                                                         const dropkv_cache_attn* attn);
+DROPKV_API dropkv_status dropkv_cache_attention(const dropkv_cache* cache,
+                                                const dropkv_cache_attn* attn, void* workspace,
+                                                size_t workspace_bytes, int32_t* status_dev,
+                                                void* stream);
+/* The path DROPKV_PATH_AUTO takes (DROPKV_PATH_SIMT or DROPKV_PATH_TENSOR); the
+ * alignment of q and out counts.  -1 for invalid sizes.  No device needed. */
+DROPKV_API int32_t dropkv_cache_attention_path(const dropkv_cache* cache,
+                                               const dropkv_cache_attn* attn);
 
 /* Which path DROPKV_PATH_AUTO picks for this shape (DROPKV_PATH_SIMT or
  * DROPKV_PATH_TENSOR); no device needed.  Returns -1 for an invalid shape. */

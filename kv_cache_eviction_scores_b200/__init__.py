@@ -21,10 +21,23 @@ Usage (CUDA tensors; q holds the last ``window`` query rows of each sequence)::
     scores, keep_idx, evict_idx = dk.evict(q, k, v, window, pool_kernel, keep_counts, lengths)
     # the attention-only control score through the same pipeline:
     control = dk.dropkv_scores(q, k, v, window, pool_kernel, lengths, score="attention")
+
+The kept rows, and the tokens after them, live in a paged cache (bf16, fp32, or
+e4m3 with a power-of-two scale per row)::
+
+    # pages [n_pages, Hkv, page_size, d], page_table int32 [B, max_pages]
+    dk.dropkv_cache_write(k, v, k_pages, v_pages, page_table, rows=keep_idx)   # kept -> slots 0..
+    dk.dropkv_cache_write(k_new, v_new, k_pages, v_pages, page_table, start=lengths)  # append
+    # q [B, Hq, T, d]: the last T of each sequence's `lengths` slots
+    out = dk.dropkv_cache_attention(q, k_pages, v_pages, page_table, lengths)
+    k, v = dk.dropkv_cache_read(k_pages, v_pages, page_table, n)               # back to dense
+    # an eviction whose kept rows go straight into a cache:
+    dk.evict_to_cache(q, k, v, window, pool_kernel, keep_counts, k_pages, v_pages, page_table)
 """
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Sequence, Tuple
@@ -34,7 +47,9 @@ import torch
 __all__ = [
     "DropKVError", "SingularError", "Shape", "Options", "lib", "lib_path",
     "make_shape", "scores_workspace_bytes", "select_workspace_bytes", "dropkv_scores",
-    "dropkv_select", "evict", "auto_path", "scores_launches", "select_launches",
+    "dropkv_select", "evict", "evict_to_cache", "dropkv_cache_write", "dropkv_cache_read",
+    "dropkv_cache_attention", "cache_attention_workspace_bytes", "cache_attention_path",
+    "Cache", "CacheRows", "CacheAttn", "auto_path", "scores_launches", "select_launches",
     "selftest_wait_timeout", "selftest_select_timeout",
     "OK", "ERR_ARG", "ERR_SINGULAR", "ERR_CUDA", "ERR_UNSUPPORTED", "ERR_WORKSPACE", "ERR_TIMEOUT",
     "PATH_AUTO", "PATH_SIMT", "PATH_TENSOR", "SCORE_PERTURBATION", "SCORE_ATTENTION",
@@ -45,7 +60,9 @@ PATH_AUTO, PATH_SIMT, PATH_TENSOR = 0, 1, 2
 _PATHS = {"auto": PATH_AUTO, "simt": PATH_SIMT, "tensor": PATH_TENSOR}
 SCORE_PERTURBATION, SCORE_ATTENTION = 0, 1
 _SCORES = {"perturbation": SCORE_PERTURBATION, "attention": SCORE_ATTENTION}
-BF16, F32 = 0, 1
+BF16, F32, E4M3 = 0, 1, 2
+_PAGE_DTYPES = {torch.bfloat16: BF16, torch.float32: F32, torch.float8_e4m3fn: E4M3}
+_DENSE_DTYPES = {torch.bfloat16: BF16, torch.float32: F32}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 
@@ -75,6 +92,29 @@ class Options(ctypes.Structure):
                 ("attn_out", ctypes.c_void_p), ("stats_out", ctypes.c_void_p),
                 ("events", ctypes.c_void_p), ("n_events", ctypes.c_int32),
                 ("tc_ctas", ctypes.c_int32)]
+
+
+class Cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("B", "Hkv", "d", "n_pages", "page_size", "max_pages", "dtype", "reserved")] + \
+               [(n, ctypes.c_void_p) for n in
+                ("k_pages", "v_pages", "k_scale", "v_scale", "page_table")]
+
+
+class CacheRows(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3),
+                ("dtype", ctypes.c_int32), ("n", ctypes.c_int32), ("m", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("rows", ctypes.c_void_p),
+                ("start", ctypes.c_void_p), ("counts", ctypes.c_void_p)]
+
+
+class CacheAttn(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64 * 3), ("out_stride", ctypes.c_int64 * 3),
+                ("dtype", ctypes.c_int32), ("Hq", ctypes.c_int32), ("T", ctypes.c_int32),
+                ("causal", ctypes.c_int32), ("scale", ctypes.c_float), ("path", ctypes.c_int32),
+                ("lengths", ctypes.c_void_p), ("q_lengths", ctypes.c_void_p)]
 
 
 _lib = None
@@ -132,6 +172,16 @@ def lib():
     L.dropkv_last_cuda_error.restype = i32
     L.dropkv_last_cuda_error_string.argtypes = []
     L.dropkv_last_cuda_error_string.restype = ctypes.c_char_p
+    cp, rp, ap = ctypes.POINTER(Cache), ctypes.POINTER(CacheRows), ctypes.POINTER(CacheAttn)
+    for fn in (L.dropkv_cache_write, L.dropkv_cache_read):
+        fn.argtypes = [cp, rp, vp, vp]
+        fn.restype = i32
+    L.dropkv_cache_attention_workspace_bytes.argtypes = [cp, ap]
+    L.dropkv_cache_attention_workspace_bytes.restype = sz
+    L.dropkv_cache_attention.argtypes = [cp, ap, vp, sz, vp, vp]
+    L.dropkv_cache_attention.restype = i32
+    L.dropkv_cache_attention_path.argtypes = [cp, ap]
+    L.dropkv_cache_attention_path.restype = i32
     _lib = L
     return L
 
@@ -417,3 +467,274 @@ def evict(q, k, v, window: int, pool_kernel: int, keep_counts: Sequence[int],
     """Scores and the keep / evict lists in one call: (scores, keep_idx, evict_idx)."""
     return dropkv_scores_select(q, k, v, window, pool_kernel, keep_counts, lengths, path=path,
                                 score=score)
+
+
+# ---- paged cache -----------------------------------------------------------------
+
+
+def _cache(k_pages, v_pages, page_table, k_scale, v_scale) -> Cache:
+    """Checks the pages' tensors and describes them to the library."""
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor (there is no CPU path)")
+        if t.dim() != 4 or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous [n_pages, Hkv, page_size, d] tensor")
+        if t.dtype not in _PAGE_DTYPES:
+            raise TypeError("pages must be bfloat16, float32 or float8_e4m3fn")
+    if k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype:
+        raise ValueError("k_pages and v_pages must have the same shape and dtype")
+    n_pages, Hkv, page_size, d = k_pages.shape
+    dt = _PAGE_DTYPES[k_pages.dtype]
+    _int32_on(page_table, "page_table", k_pages.device)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if (t is not None) != (dt == E4M3):
+            raise ValueError("e4m3 pages come with k_scale and v_scale, other pages without")
+        if t is None:
+            continue
+        if t.dtype != torch.uint8 or t.device != k_pages.device or not t.is_contiguous():
+            raise TypeError(f"{name} must be a contiguous uint8 tensor on the pages' device")
+        if t.shape != k_pages.shape[:3]:
+            raise ValueError(f"{name} must be [n_pages, Hkv, page_size]")
+    return Cache(page_table.shape[0], Hkv, d, n_pages, page_size, page_table.shape[1], dt, 0,
+                 k_pages.data_ptr(), v_pages.data_ptr(),
+                 None if k_scale is None else k_scale.data_ptr(),
+                 None if v_scale is None else v_scale.data_ptr(), page_table.data_ptr())
+
+
+def _int32_on(t, name, device, shape=None):
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != device:
+        raise TypeError(f"{name} must be an int32 tensor on the pages' device")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have the shape {list(shape)}")
+    return t.data_ptr()
+
+
+def _dense(t, name, device, shape):
+    """Strides of a dense bf16 / fp32 tensor whose last index is contiguous."""
+    if not isinstance(t, torch.Tensor) or t.device != device:
+        raise TypeError(f"{name} must be a CUDA tensor on the pages' device")
+    if t.dtype not in _DENSE_DTYPES:
+        raise TypeError(f"{name} must be bfloat16 or float32")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have the shape {list(shape)}")
+    st = t.stride()
+    if st[3] != 1 and shape[3] != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    return (ctypes.c_int64 * 3)(*st[:3])
+
+
+def _written(t, name):
+    """A tensor that a call writes: no element may stand for two indices."""
+    reach = 1
+    for size, stride in sorted(((n, s) for n, s in zip(t.shape, t.stride()) if n > 1),
+                               key=lambda x: x[1]):
+        if stride < reach:
+            raise ValueError(f"{name} must not overlap itself")
+        reach = stride * size
+
+
+@contextlib.contextmanager
+def _reported(device, status, sync, what):
+    """The device of a call and its status word; after it, with ``sync``, the
+    wait and the check."""
+    if status is not None and (not status.is_cuda or status.dtype != torch.int32):
+        raise TypeError("status must be a CUDA int32 tensor")
+    if sync and status is None:
+        status = torch.empty(1, dtype=torch.int32, device=device)
+    if device.index == torch.cuda.current_device():
+        yield status
+    else:
+        with torch.cuda.device(device):
+            yield status
+    if sync:
+        torch.cuda.current_stream(device).synchronize()
+        _check(int(status[0].item()), what)
+
+
+def _move(fn, what, dense, pages, shape, rows, start, counts, status, sync):
+    k, v, (k_pages, v_pages, page_table, k_scale, v_scale) = *dense, pages
+    c = _cache(k_pages, v_pages, page_table, k_scale, v_scale)
+    dev = k_pages.device
+    n = shape[2]
+    m = n if rows is None else rows.shape[-1]
+    ks, vs = _dense(k, "k", dev, shape), _dense(v, "v", dev, shape)
+    if k.dtype != v.dtype:
+        raise TypeError("k and v must share one dtype")
+    r = CacheRows(k.data_ptr(), v.data_ptr(), ks, vs, _DENSE_DTYPES[k.dtype], n, m, 0,
+                  _int32_on(rows, "rows", dev, (c.B, c.Hkv, m)),
+                  _int32_on(start, "start", dev, (c.B,)),
+                  _int32_on(counts, "counts", dev, (c.B,)))
+    if m == 0 or n == 0:  # nothing to move
+        if status is not None:
+            status.zero_()
+        return
+    with _reported(dev, status, sync, what) as word:
+        _check(fn(ctypes.byref(c), ctypes.byref(r), _ptr(word), _stream(dev)), what)
+
+
+def dropkv_cache_write(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor,
+                       v_pages: torch.Tensor, page_table: torch.Tensor, *,
+                       rows: Optional[torch.Tensor] = None, start: Optional[torch.Tensor] = None,
+                       counts: Optional[torch.Tensor] = None,
+                       k_scale: Optional[torch.Tensor] = None,
+                       v_scale: Optional[torch.Tensor] = None,
+                       status: Optional[torch.Tensor] = None, sync: bool = False) -> None:
+    """Writes dense K/V rows into a paged cache (dropkv_cache_write).
+
+    k, v: [B, Hkv, n, d], bf16 or fp32, any strides with a contiguous last
+    dimension (a transposed [B, n, Hkv, d] is fine).  k_pages, v_pages:
+    [n_pages, Hkv, page_size, d] in bf16, fp32 or float8_e4m3fn, the last with
+    uint8 scales k_scale, v_scale [n_pages, Hkv, page_size] (2^(byte - 127) a
+    row).  page_table: int32 [B, max_pages].
+    Slot start[b] + i of sequence b receives row i, or row rows[b, h, i] of a
+    list (int32 [B, Hkv, m], such as dropkv_select's keep_idx; -1 is skipped),
+    for i < counts[b].  start and counts: int32 [B] on the device, None for 0
+    and for all rows.
+    Asynchronous.  With ``status`` (a CUDA int32 tensor of one element) the
+    device-side status lands there (ERR_ARG: some page, slot, row or count was
+    out of range; what it named was left out); ``sync=True`` waits and raises.
+    """
+    B, Hkv, n, d = page_table.shape[0], k_pages.shape[1], k.shape[2], k_pages.shape[3]
+    _move(lib().dropkv_cache_write, "dropkv_cache_write", (k, v),
+          (k_pages, v_pages, page_table, k_scale, v_scale), (B, Hkv, n, d), rows, start, counts,
+          status, sync)
+
+
+def dropkv_cache_read(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
+                      n: int, *, rows: Optional[torch.Tensor] = None,
+                      start: Optional[torch.Tensor] = None,
+                      counts: Optional[torch.Tensor] = None,
+                      k_scale: Optional[torch.Tensor] = None,
+                      v_scale: Optional[torch.Tensor] = None, dtype: Optional[torch.dtype] = None,
+                      out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
+                      status: Optional[torch.Tensor] = None, sync: bool = False):
+    """Dense (k, v) [B, Hkv, n, d] of a paged cache (dropkv_cache_read).
+
+    Row i is slot start[b] + i of sequence b, or slot start[b] + rows[b, h, i]
+    of a list (int32 [B, Hkv, n]; -1 is skipped), for i < counts[b].  Rows that
+    are not written keep ``out``'s values, or are 0 without ``out``.  ``dtype``:
+    bf16 or fp32 (default: the pages' own, bf16 for e4m3 pages).  The other
+    arguments are dropkv_cache_write's.
+    """
+    B, Hkv, d = page_table.shape[0], k_pages.shape[1], k_pages.shape[3]
+    if rows is not None and rows.shape[-1] != n:
+        raise ValueError("rows must list n slots per (sequence, head)")
+    if out is None:
+        dtype = dtype or (k_pages.dtype if k_pages.dtype in _DENSE_DTYPES else torch.bfloat16)
+        out = tuple(torch.zeros(B, Hkv, n, d, dtype=dtype, device=k_pages.device)
+                    for _ in range(2))
+    else:
+        for name, t in zip(("k", "v"), out):
+            _written(t, f"out {name}")
+            if dtype is not None and t.dtype != dtype:
+                raise TypeError("out and dtype disagree")
+    _move(lib().dropkv_cache_read, "dropkv_cache_read", out,
+          (k_pages, v_pages, page_table, k_scale, v_scale), (B, Hkv, n, d), rows, start, counts,
+          status, sync)
+    return out
+
+
+def cache_attention_workspace_bytes(cache: Cache, attn: CacheAttn) -> int:
+    return int(lib().dropkv_cache_attention_workspace_bytes(ctypes.byref(cache),
+                                                            ctypes.byref(attn)))
+
+
+def cache_attention_path(cache: Cache, attn: CacheAttn) -> int:
+    return int(lib().dropkv_cache_attention_path(ctypes.byref(cache), ctypes.byref(attn)))
+
+
+def dropkv_cache_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                           page_table: torch.Tensor, lengths: torch.Tensor, *,
+                           q_lengths: Optional[torch.Tensor] = None,
+                           scale: Optional[float] = None, causal: bool = True,
+                           k_scale: Optional[torch.Tensor] = None,
+                           v_scale: Optional[torch.Tensor] = None,
+                           out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                           return_lse: bool = False, path: str = "auto",
+                           workspace: Optional[torch.Tensor] = None,
+                           status: Optional[torch.Tensor] = None, sync: bool = False):
+    """Attention of a chunk of new tokens over a paged cache
+    (dropkv_cache_attention): out [B, Hq, T, d], or (out, lse).
+
+    q: [B, Hq, T, d], bf16 or fp32, any strides with a contiguous last
+    dimension.  lengths: int32 [B] on the device, the slots of each sequence
+    with the chunk's own tokens (written beforehand) as the last ones.
+    q_lengths: int32 [B], the tokens of each chunk (None: T); rows behind them
+    keep ``out``'s and ``lse``'s values (0 without ``out`` / ``lse``).  Row t
+    sees the slots up to its own position, all of them with ``causal=False``.
+    A row that sees nothing gives 0 and a log-sum-exp of -inf.  ``scale``:
+    default 1/sqrt(d).  ``lse``: fp32 [B, Hq, T], natural logarithm; returned
+    with ``return_lse`` or when given.  ``path``: "auto", "simt" (fp32 CUDA
+    cores) or "tensor".  The other arguments are dropkv_cache_write's.
+    """
+    c = _cache(k_pages, v_pages, page_table, k_scale, v_scale)
+    dev = k_pages.device
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be [B, Hq, T, d]")
+    B, Hq, T, d = q.shape
+    if (B, d) != (c.B, c.d) or Hq % c.Hkv:
+        raise ValueError("q must be [B, Hq, T, d] with the pages' B and d and Hq a multiple of Hkv")
+    qs = _dense(q, "q", dev, q.shape)
+    if out is None:
+        out = torch.zeros(q.shape, dtype=q.dtype, device=dev) if q_lengths is not None else \
+            torch.empty(q.shape, dtype=q.dtype, device=dev)
+    os_ = _dense(out, "out", dev, q.shape)
+    _written(out, "out")
+    if out.dtype != q.dtype:
+        raise TypeError("out must have q's dtype")
+    if lse is not None:
+        if lse.dtype != torch.float32 or lse.device != dev or not lse.is_contiguous() \
+                or tuple(lse.shape) != (B, Hq, T):
+            raise ValueError("lse must be a contiguous fp32 [B, Hq, T] tensor on the pages' device")
+        return_lse = True
+    elif return_lse:
+        lse = torch.zeros(B, Hq, T, device=dev)
+    if scale is not None and not (0.0 < scale < float("inf")):
+        raise ValueError("scale must be positive and finite")
+    if lengths is None:
+        raise ValueError("lengths are needed")
+    a = CacheAttn(q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(), qs, os_,
+                  _DENSE_DTYPES[q.dtype], Hq, T, 1 if causal else 0, scale or 0.0, _PATHS[path],
+                  _int32_on(lengths, "lengths", dev, (B,)),
+                  _int32_on(q_lengths, "q_lengths", dev, (B,)))
+    if T == 0:  # no rows
+        if status is not None:
+            status.zero_()
+        return (out, lse) if return_lse else out
+    need = cache_attention_workspace_bytes(c, a)
+    if need == 0:
+        raise DropKVError(ERR_ARG, "dropkv_cache_attention_workspace_bytes")
+    if workspace is None or workspace.numel() * workspace.element_size() < need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    with _reported(dev, status, sync, "dropkv_cache_attention") as word:
+        _check(lib().dropkv_cache_attention(ctypes.byref(c), ctypes.byref(a), _ptr(workspace),
+                                            workspace.numel() * workspace.element_size(),
+                                            _ptr(word), _stream(dev)), "dropkv_cache_attention")
+    return (out, lse) if return_lse else out
+
+
+def evict_to_cache(q, k, v, window: int, pool_kernel: int, keep_counts: Sequence[int],
+                   k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
+                   lengths: Optional[Sequence[int]] = None, *,
+                   k_scale: Optional[torch.Tensor] = None,
+                   v_scale: Optional[torch.Tensor] = None, path: str = "auto",
+                   score: str = "perturbation"):
+    """Scores the prompt's tokens, lists the kept ones, and writes their K/V rows
+    into slots 0.. of a paged cache: (cache lengths int32 [B], scores, keep_idx,
+    evict_idx).  The arguments are evict's and dropkv_cache_write's."""
+    _cache(k_pages, v_pages, page_table, k_scale, v_scale)  # refuse before any work
+    keep = [int(x) for x in keep_counts]
+    if keep and max(keep) > page_table.shape[1] * k_pages.shape[2]:
+        raise ValueError("the page table has too few pages for the kept tokens")
+    scores, keep_idx, evict_idx = evict(q, k, v, window, pool_kernel, keep, lengths, path=path,
+                                        score=score)
+    counts = torch.tensor(keep, dtype=torch.int32, device=q.device)
+    dropkv_cache_write(k, v, k_pages, v_pages, page_table, rows=keep_idx, counts=counts,
+                       k_scale=k_scale, v_scale=v_scale, sync=True)
+    return counts, scores, keep_idx, evict_idx

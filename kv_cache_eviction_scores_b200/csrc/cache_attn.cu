@@ -1,0 +1,112 @@
+// cache_attn.cu -- dropkv_cache_attention's entry points: argument checks, the
+// choice of the path, the workspace and the launches.
+#include <math.h>
+
+#include <algorithm>
+
+#include "cache_attn.cuh"
+
+namespace dropkv {
+
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+dropkv_status check_attn(const dropkv_cache* c, const dropkv_cache_attn* t, bool pointers) {
+  dropkv_status s = check_cache(c, pointers);
+  if (s != DROPKV_OK) return s;
+  if (!t || t->Hq < 1 || t->Hq % c->Hkv != 0 || t->T < 1) return DROPKV_ERR_ARG;
+  if (t->dtype != DROPKV_BF16 && t->dtype != DROPKV_F32) return DROPKV_ERR_ARG;
+  if (t->causal != 0 && t->causal != 1) return DROPKV_ERR_ARG;
+  if (!(t->scale >= 0.f) || isinf(t->scale)) return DROPKV_ERR_ARG;
+  if (t->path != DROPKV_PATH_AUTO && t->path != DROPKV_PATH_SIMT && t->path != DROPKV_PATH_TENSOR)
+    return DROPKV_ERR_ARG;
+  // rows of a group and (sequence, row tile) items are 32-bit
+  if ((double)(t->Hq / c->Hkv) * t->T > 1.0e9) return DROPKV_ERR_ARG;
+  if ((double)c->B * (t->Hq / c->Hkv) * t->T > 1.6e10) return DROPKV_ERR_ARG;
+  for (int i = 0; i < 3; ++i)
+    if (t->q_stride[i] < 0 || t->out_stride[i] < 0) return DROPKV_ERR_ARG;
+  if (!pointers) return DROPKV_OK;
+  const int esz = t->dtype == DROPKV_BF16 ? 2 : 4;
+  if (!t->q || !t->out || !t->lengths) return DROPKV_ERR_ARG;
+  if (((uintptr_t)t->q | (uintptr_t)t->out) % esz) return DROPKV_ERR_ARG;
+  if (((uintptr_t)t->lse | (uintptr_t)t->lengths | (uintptr_t)t->q_lengths) & 3u)
+    return DROPKV_ERR_ARG;
+  return DROPKV_OK;
+}
+
+size_t layout(const dropkv_cache& c, const AttnGrid& g, size_t* part) {
+  const size_t desc = align_up((size_t)g.ctas * sizeof(int4), 256);
+  if (part) *part = desc;
+  return desc + (size_t)2 * g.ctas * g.rows * ((c.d + 3) / 4 * 4 + 4) * sizeof(float);
+}
+
+}  // namespace
+
+}  // namespace dropkv
+
+using namespace dropkv;
+
+extern "C" size_t dropkv_cache_attention_workspace_bytes(const dropkv_cache* cache,
+                                                         const dropkv_cache_attn* attn) {
+  if (check_attn(cache, attn, false) != DROPKV_OK) return 0;
+  return layout(*cache, attn_grid_general(*cache, *attn), nullptr);
+}
+
+extern "C" int32_t dropkv_cache_attention_path(const dropkv_cache* cache,
+                                               const dropkv_cache_attn* attn) {
+  if (check_attn(cache, attn, false) != DROPKV_OK) return -1;
+  return DROPKV_PATH_SIMT;
+}
+
+extern "C" dropkv_status dropkv_cache_attention(const dropkv_cache* cache,
+                                                const dropkv_cache_attn* attn, void* workspace,
+                                                size_t workspace_bytes, int32_t* status_dev,
+                                                void* stream) {
+  NvtxRange range("dropkv_cache_attention");
+  dropkv_status s = check_attn(cache, attn, true);
+  if (s != DROPKV_OK) return s;
+  const dropkv_cache& c = *cache;
+  const dropkv_cache_attn& t = *attn;
+  if ((uintptr_t)status_dev & 3u) return DROPKV_ERR_ARG;
+  const int path = DROPKV_PATH_SIMT;
+  if (t.path == DROPKV_PATH_TENSOR && path != DROPKV_PATH_TENSOR) return DROPKV_ERR_UNSUPPORTED;
+  if (!workspace || !aligned16(workspace) ||
+      workspace_bytes < dropkv_cache_attention_workspace_bytes(cache, attn))
+    return DROPKV_ERR_WORKSPACE;
+  s = device_ok();
+  if (s != DROPKV_OK) return s;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (status_dev)
+    if (cudaError_t e = cudaMemsetAsync(status_dev, 0, sizeof(int32_t), st)) return cuda_fail(e);
+
+  const AttnGrid g = attn_grid_general(c, t);
+  AttnDev a = {};
+  a.c = cache_dev(c);
+  a.q = t.q;
+  a.out = t.out;
+  a.lse = t.lse;
+  for (int i = 0; i < 3; ++i) {
+    a.qs[i] = t.q_stride[i];
+    a.os[i] = t.out_stride[i];
+  }
+  a.Hq = t.Hq;
+  a.G = t.Hq / c.Hkv;
+  a.T = t.T;
+  a.causal = t.causal;
+  a.fG = FastDiv::of((uint32_t)a.G);
+  a.nrt = (a.G * t.T + g.rows - 1) / g.rows;
+  const double scale = t.scale > 0.f ? (double)t.scale : 1.0 / sqrt((double)c.d);
+  a.c_log2 = (float)(scale * 1.4426950408889634);
+  a.lengths = t.lengths;
+  a.q_lengths = t.q_lengths;
+  size_t part;
+  layout(c, g, &part);
+  a.desc = reinterpret_cast<int4*>(workspace);
+  a.part = reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) + part);
+  a.pstride = (c.d + 3) / 4 * 4 + 4;
+  a.status = status_dev;
+  cudaError_t e = launch_attn_general(a, c.dtype, t.dtype, st);
+  if (e == cudaSuccess) e = launch_attn_merge(a, g.ctas, g.rows, t.dtype, st);
+  return e == cudaSuccess ? DROPKV_OK : cuda_fail(e);
+}

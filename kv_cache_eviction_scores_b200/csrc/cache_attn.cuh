@@ -1,0 +1,229 @@
+// cache_attn.cuh -- what the cache attention kernels share: the arguments, the
+// split of the work over the CTAs, and a row's last step.
+//
+// Work split.  A unit is (sequence b, row tile, KV head h): up to kRows of the
+// group's G * q_len query rows (row r is token r / G of query head h G + r % G,
+// so that a tile covers few tokens and a causal tile stops early) against the
+// slots they see, in tiles of kTile slots.  The units' tiles, laid end to end,
+// are cut into one equal range per CTA, so that ragged lengths leave no CTA
+// behind; the lengths are device data, so every CTA finds its range itself
+// with one scan over the (b, row tile) items.  A unit that lies within one
+// range is finished there; a unit that is cut leaves one partial per CTA (the
+// unnormalised O, the reference maximum m and the sum l of each row), which
+// k_attn_merge joins in the order of the slots.
+#pragma once
+
+#include "cache.cuh"
+
+namespace dropkv {
+
+struct AttnDev {
+  CacheDev c;
+  const void* q;
+  void* out;
+  float* lse;
+  int64_t qs[3], os[3];
+  int32_t Hq, G, T, causal;
+  FastDiv fG;
+  int32_t nrt;      // row tiles a sequence can have: ceil(G T / kRows)
+  float c_log2;     // scale * log2(e)
+  const int32_t* lengths;
+  const int32_t* q_lengths;
+  float* part;      // [2 grid][rows][pstride]
+  int4* desc;       // [grid][2]: the cut unit that begins in a CTA
+  int32_t pstride;  // floats of a partial row: O (d rounded up to 4), m, l, pad
+  int32_t* status;
+};
+
+// ex2 and the row statistics are in units of log2.
+__device__ __forceinline__ float attn_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Sequence b's slots and chunk, clamped to what there is.
+__device__ __forceinline__ void attn_lengths(const AttnDev& a, int b, int& L, int& n) {
+  L = __ldg(a.lengths + b);
+  n = a.q_lengths ? __ldg(a.q_lengths + b) : a.T;
+  if ((uint32_t)L > (uint32_t)a.c.cap || (uint32_t)n > (uint32_t)a.T) {
+    raise_arg(a.status);
+    L = min(max(L, 0), a.c.cap);
+    n = min(max(n, 0), a.T);
+  }
+}
+// Slots that row r (token r / G) sees.
+__device__ __forceinline__ int attn_seen(const AttnDev& a, int L, int n, int r) {
+  return a.causal ? max(0, L - n + (int)a.fG.div((uint32_t)r) + 1) : L;
+}
+// Tiles of a unit of item (b, rt): those of its last row, and one at least, so
+// that rows that see nothing are written too; 0 if the item has no rows.
+template <int kRows, int kTile>
+__device__ __forceinline__ int attn_tiles(const AttnDev& a, int item) {
+  const int b = item / a.nrt, rt = item - b * a.nrt;
+  int L, n;
+  attn_lengths(a, b, L, n);
+  const int rows = a.G * n;
+  if (rt * kRows >= rows) return 0;
+  const int seen = attn_seen(a, L, n, min((rt + 1) * kRows, rows) - 1);
+  return max(1, (seen + kTile - 1) / kTile);
+}
+
+// A CTA's place in the work: item, head, the tiles [t0, t1) of the unit's `nt`
+// that belong to the CTA, and what is left of the CTA's range after the unit.
+struct AttnWalk {
+  int item, h, nt, t0, t1;
+  int64_t g0;        // first tile of the unit among all tiles
+  int64_t left;      // tiles of the range from t0 on
+};
+
+struct AttnPlanShared {
+  int64_t warp_sum[33];
+  int64_t g0;        // of the item
+  int item, nt;
+};
+
+// The range of this CTA (kThreads threads, all call it).  total and grid: all
+// tiles and the CTAs that have a range (every one of them a non-empty one).
+template <int kRows, int kTile, int kThreads>
+__device__ __forceinline__ bool attn_plan(const AttnDev& a, AttnPlanShared& sh, AttnWalk& w,
+                                          int64_t& total, int& grid) {
+  constexpr int kWarps = kThreads / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int items = a.c.B * a.nrt;
+  // pass 1: all tiles; with no more items than threads its scan also places
+  // the range
+  int64_t sum = 0, incl = 0, base = 0;
+  int mine = 0;
+  for (int i0 = 0; i0 < items; i0 += kThreads) {
+    const int it = i0 + (int)threadIdx.x;
+    mine = it < items ? attn_tiles<kRows, kTile>(a, it) : 0;
+    sum += (int64_t)mine * a.c.Hkv;
+  }
+  incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) sh.warp_sum[warp] = incl;
+  __syncthreads();
+  total = 0;
+  for (int i = 0; i < kWarps; ++i) {
+    if (i == warp) base = total;
+    total += sh.warp_sum[i];
+  }
+  grid = (int)min((int64_t)gridDim.x, total);
+  if ((int)blockIdx.x >= grid) return false;
+  const int64_t first = total * blockIdx.x / grid, last = total * (blockIdx.x + 1) / grid;
+  if (items <= kThreads) {
+    const int64_t e = base + incl - sum;  // tiles before this thread's item
+    if (first >= e && first < e + sum) {
+      sh.item = threadIdx.x;
+      sh.nt = mine;
+      sh.g0 = e;
+    }
+    __syncthreads();
+  } else {
+    // pass 2: the same scan chunk by chunk until the range's first tile
+    int64_t before = 0;
+    for (int i0 = 0; i0 < items; i0 += kThreads) {
+      const int it = i0 + (int)threadIdx.x;
+      const int nt = it < items ? attn_tiles<kRows, kTile>(a, it) : 0;
+      const int64_t own = (int64_t)nt * a.c.Hkv;
+      int64_t s = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += x;
+      }
+      __syncthreads();
+      if (lane == 31) sh.warp_sum[warp] = s;
+      __syncthreads();
+      int64_t all = 0, wb = 0;
+      for (int i = 0; i < kWarps; ++i) {
+        if (i == warp) wb = all;
+        all += sh.warp_sum[i];
+      }
+      const int64_t e = before + wb + s - own;
+      if (first >= e && first < e + own) {
+        sh.item = it;
+        sh.nt = nt;
+        sh.g0 = e;
+      }
+      before += all;
+      if (first < before) break;  // the same for every thread
+    }
+    __syncthreads();
+  }
+  w.item = sh.item;
+  w.nt = sh.nt;
+  const int64_t in_item = first - sh.g0;
+  w.h = (int)(in_item / w.nt);
+  w.t0 = (int)(in_item - (int64_t)w.h * w.nt);
+  w.g0 = sh.g0 + (int64_t)w.h * w.nt;
+  w.left = last - first;
+  w.t1 = (int)min((int64_t)w.nt, w.t0 + w.left);
+  return true;
+}
+
+// The next unit of the range; false at its end.
+template <int kRows, int kTile>
+__device__ __forceinline__ bool attn_next(const AttnDev& a, AttnWalk& w) {
+  w.left -= w.t1 - w.t0;
+  if (w.left <= 0) return false;
+  w.g0 += w.nt;
+  if (++w.h == a.c.Hkv) {
+    w.h = 0;
+    do {
+      ++w.item;
+      w.nt = attn_tiles<kRows, kTile>(a, w.item);
+    } while (w.nt == 0);
+  }
+  w.t0 = 0;
+  w.t1 = (int)min((int64_t)w.nt, w.left);
+  return true;
+}
+
+// Where the unit's rows go: -1 to the output (the unit is whole), or the
+// partial's slot: 2 cta + 1 for the unit that begins in the CTA and does not
+// end there, 2 cta for the one that began in an earlier CTA.
+__device__ __forceinline__ int attn_slot(const AttnWalk& w) {
+  if (w.t0 == 0 && w.t1 == w.nt) return -1;
+  return 2 * (int)blockIdx.x + (w.t0 == 0 ? 1 : 0);
+}
+// Records the cut unit that begins in this CTA for the merge (one thread).
+__device__ __forceinline__ void attn_describe(const AttnDev& a, const AttnWalk& w, int64_t total,
+                                              int grid) {
+  const int64_t end = w.g0 + w.nt - 1;
+  const int c1 = (int)(((end + 1) * grid - 1) / total);  // the CTA of its last tile
+  a.desc[blockIdx.x] = make_int4(w.item, w.h, c1, 0);
+}
+
+// A row's output position.
+struct AttnRow {
+  int b, hq, t;
+};
+__device__ __forceinline__ AttnRow attn_row(const AttnDev& a, int b, int h, int r) {
+  AttnRow x;
+  x.b = b;
+  x.t = (int)a.fG.div((uint32_t)r);
+  x.hq = h * a.G + (r - x.t * a.G);
+  return x;
+}
+__device__ __forceinline__ void attn_put_lse(const AttnDev& a, const AttnRow& x, float m, float l) {
+  if (a.lse)
+    a.lse[((int64_t)x.b * a.Hq + x.hq) * a.T + x.t] =
+        l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : (l == 0.f ? -CUDART_INF_F : l);
+}
+
+struct AttnGrid {
+  int ctas;
+  int rows;
+};
+// Grid and unit rows of each kernel (host); launchers of one call's kernels.
+AttnGrid attn_grid_general(const dropkv_cache& c, const dropkv_cache_attn& t);
+cudaError_t launch_attn_general(AttnDev a, int page_dtype, int q_dtype, cudaStream_t st);
+cudaError_t launch_attn_merge(const AttnDev& a, int ctas, int rows, int q_dtype, cudaStream_t st);
+
+}  // namespace dropkv

@@ -174,4 +174,9 @@ dropkv_status run_select(int32_t B, int32_t Hkv, int32_t n_max, const float* sco
                          int32_t* status_word, cudaStream_t st);
 dropkv_status cuda_fail(cudaError_t e);
 
+// ---- paged cache --------------------------------------------------------------
+// Host-side checks of the pages' description; without `pointers`, of its sizes
+// alone.
+dropkv_status check_cache(const dropkv_cache* c, bool pointers);
+
 }  // namespace dropkv
