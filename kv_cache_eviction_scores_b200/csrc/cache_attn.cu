@@ -35,6 +35,25 @@ dropkv_status check_attn(const dropkv_cache* c, const dropkv_cache_attn* t, bool
   return DROPKV_OK;
 }
 
+// The tensor path's sizes: pool rows that fit 32 bits, and the types and head
+// dims its kernels are built for.
+bool tensor_sizes(const dropkv_cache& c, const dropkv_cache_attn& t) {
+  return t.dtype == DROPKV_BF16 && (c.dtype == DROPKV_BF16 || c.dtype == DROPKV_E4M3) &&
+         (c.d == 64 || c.d == 128) &&
+         (double)c.n_pages * c.Hkv * c.page_size < 2147483648.0;
+}
+// 16-byte loads of q and stores of out
+bool tensor_aligned(const dropkv_cache_attn& t) {
+  bool ok = aligned16(t.q) && aligned16(t.out);
+  for (int i = 0; i < 3; ++i) ok = ok && t.q_stride[i] % 8 == 0 && t.out_stride[i] % 8 == 0;
+  return ok;
+}
+int path_of(const dropkv_cache& c, const dropkv_cache_attn& t) {
+  if (t.path == DROPKV_PATH_SIMT) return DROPKV_PATH_SIMT;
+  if (tensor_sizes(c, t) && tensor_aligned(t)) return DROPKV_PATH_TENSOR;
+  return t.path == DROPKV_PATH_TENSOR ? -1 : DROPKV_PATH_SIMT;
+}
+
 size_t layout(const dropkv_cache& c, const AttnGrid& g, size_t* part) {
   const size_t desc = align_up((size_t)g.ctas * sizeof(int4), 256);
   if (part) *part = desc;
@@ -50,13 +69,17 @@ using namespace dropkv;
 extern "C" size_t dropkv_cache_attention_workspace_bytes(const dropkv_cache* cache,
                                                          const dropkv_cache_attn* attn) {
   if (check_attn(cache, attn, false) != DROPKV_OK) return 0;
-  return layout(*cache, attn_grid_general(*cache, *attn), nullptr);
+  // the alignment of q and out is not known here: enough for either path
+  const size_t simt = layout(*cache, attn_grid_simt(), nullptr);
+  if (attn->path == DROPKV_PATH_SIMT || !tensor_sizes(*cache, *attn)) return simt;
+  const size_t tensor = layout(*cache, attn_grid_rows(), nullptr);
+  return std::max(simt, tensor);
 }
 
 extern "C" int32_t dropkv_cache_attention_path(const dropkv_cache* cache,
                                                const dropkv_cache_attn* attn) {
   if (check_attn(cache, attn, false) != DROPKV_OK) return -1;
-  return DROPKV_PATH_SIMT;
+  return path_of(*cache, *attn);
 }
 
 extern "C" dropkv_status dropkv_cache_attention(const dropkv_cache* cache,
@@ -69,8 +92,8 @@ extern "C" dropkv_status dropkv_cache_attention(const dropkv_cache* cache,
   const dropkv_cache& c = *cache;
   const dropkv_cache_attn& t = *attn;
   if ((uintptr_t)status_dev & 3u) return DROPKV_ERR_ARG;
-  const int path = DROPKV_PATH_SIMT;
-  if (t.path == DROPKV_PATH_TENSOR && path != DROPKV_PATH_TENSOR) return DROPKV_ERR_UNSUPPORTED;
+  const int path = path_of(c, t);
+  if (path < 0) return DROPKV_ERR_UNSUPPORTED;
   if (!workspace || !aligned16(workspace) ||
       workspace_bytes < dropkv_cache_attention_workspace_bytes(cache, attn))
     return DROPKV_ERR_WORKSPACE;
@@ -80,7 +103,8 @@ extern "C" dropkv_status dropkv_cache_attention(const dropkv_cache* cache,
   if (status_dev)
     if (cudaError_t e = cudaMemsetAsync(status_dev, 0, sizeof(int32_t), st)) return cuda_fail(e);
 
-  const AttnGrid g = attn_grid_general(c, t);
+  const bool tensor = path == DROPKV_PATH_TENSOR;
+  const AttnGrid g = tensor ? attn_grid_rows() : attn_grid_simt();
   AttnDev a = {};
   a.c = cache_dev(c);
   a.q = t.q;
@@ -106,7 +130,8 @@ extern "C" dropkv_status dropkv_cache_attention(const dropkv_cache* cache,
   a.part = reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) + part);
   a.pstride = (c.d + 3) / 4 * 4 + 4;
   a.status = status_dev;
-  cudaError_t e = launch_attn_general(a, c.dtype, t.dtype, st);
+  cudaError_t e = tensor ? launch_attn_rows(a, c.dtype, st)
+                         : launch_attn_simt(a, c.dtype, t.dtype, st);
   if (e == cudaSuccess) e = launch_attn_merge(a, g.ctas, g.rows, t.dtype, st);
   return e == cudaSuccess ? DROPKV_OK : cuda_fail(e);
 }

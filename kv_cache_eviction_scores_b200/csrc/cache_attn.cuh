@@ -222,8 +222,10 @@ struct AttnGrid {
   int rows;
 };
 // Grid and unit rows of each kernel (host); launchers of one call's kernels.
-AttnGrid attn_grid_general(const dropkv_cache& c, const dropkv_cache_attn& t);
-cudaError_t launch_attn_general(AttnDev a, int page_dtype, int q_dtype, cudaStream_t st);
+AttnGrid attn_grid_simt();
+AttnGrid attn_grid_rows();
+cudaError_t launch_attn_simt(const AttnDev& a, int page_dtype, int q_dtype, cudaStream_t st);
+cudaError_t launch_attn_rows(const AttnDev& a, int page_dtype, cudaStream_t st);
 cudaError_t launch_attn_merge(const AttnDev& a, int ctas, int rows, int q_dtype, cudaStream_t st);
 
 }  // namespace dropkv

@@ -295,11 +295,9 @@ cudaError_t launch_simt(const AttnDev& a, cudaStream_t st) {
 
 }  // namespace
 
-AttnGrid attn_grid_general(const dropkv_cache&, const dropkv_cache_attn&) {
-  return {kSCtas, kSRows};
-}
+AttnGrid attn_grid_simt() { return {kSCtas, kSRows}; }
 
-cudaError_t launch_attn_general(AttnDev a, int page_dtype, int q_dtype, cudaStream_t st) {
+cudaError_t launch_attn_simt(const AttnDev& a, int page_dtype, int q_dtype, cudaStream_t st) {
   if (q_dtype == DROPKV_BF16) {
     if (page_dtype == DROPKV_BF16) return launch_simt<__nv_bfloat16, __nv_bfloat16>(a, st);
     if (page_dtype == DROPKV_F32) return launch_simt<__nv_bfloat16, float>(a, st);
