@@ -54,6 +54,17 @@ int path_of(const dropkv_cache& c, const dropkv_cache_attn& t) {
   return t.path == DROPKV_PATH_TENSOR ? -1 : DROPKV_PATH_SIMT;
 }
 
+// The tensor path's kernel by the rows a KV head can have: one block of the
+// row kernel, or query tiles of 128 rows.
+enum class Tensor { kRows, kTile128, kTile256 };
+Tensor tensor_of(const dropkv_cache& c, const dropkv_cache_attn& t) {
+  const int64_t rows = (int64_t)(t.Hq / c.Hkv) * t.T;
+  return rows <= 16 ? Tensor::kRows : rows <= 128 ? Tensor::kTile128 : Tensor::kTile256;
+}
+AttnGrid grid_of(Tensor k) {
+  return k == Tensor::kRows ? attn_grid_rows() : attn_grid_tile(k == Tensor::kTile128);
+}
+
 size_t layout(const dropkv_cache& c, const AttnGrid& g, size_t* part) {
   const size_t desc = align_up((size_t)g.ctas * sizeof(int4), 256);
   if (part) *part = desc;
@@ -72,7 +83,7 @@ extern "C" size_t dropkv_cache_attention_workspace_bytes(const dropkv_cache* cac
   // the alignment of q and out is not known here: enough for either path
   const size_t simt = layout(*cache, attn_grid_simt(), nullptr);
   if (attn->path == DROPKV_PATH_SIMT || !tensor_sizes(*cache, *attn)) return simt;
-  const size_t tensor = layout(*cache, attn_grid_rows(), nullptr);
+  const size_t tensor = layout(*cache, grid_of(tensor_of(*cache, *attn)), nullptr);
   return std::max(simt, tensor);
 }
 
@@ -104,7 +115,8 @@ extern "C" dropkv_status dropkv_cache_attention(const dropkv_cache* cache,
     if (cudaError_t e = cudaMemsetAsync(status_dev, 0, sizeof(int32_t), st)) return cuda_fail(e);
 
   const bool tensor = path == DROPKV_PATH_TENSOR;
-  const AttnGrid g = tensor ? attn_grid_rows() : attn_grid_simt();
+  const Tensor kind = tensor_of(c, t);
+  const AttnGrid g = tensor ? grid_of(kind) : attn_grid_simt();
   AttnDev a = {};
   a.c = cache_dev(c);
   a.q = t.q;
@@ -130,8 +142,13 @@ extern "C" dropkv_status dropkv_cache_attention(const dropkv_cache* cache,
   a.part = reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) + part);
   a.pstride = (c.d + 3) / 4 * 4 + 4;
   a.status = status_dev;
-  cudaError_t e = tensor ? launch_attn_rows(a, c.dtype, st)
-                         : launch_attn_simt(a, c.dtype, t.dtype, st);
+  cudaError_t e;
+  if (!tensor)
+    e = launch_attn_simt(a, c.dtype, t.dtype, st);
+  else if (kind == Tensor::kRows)
+    e = launch_attn_rows(a, c.dtype, st);
+  else
+    e = launch_attn_tile(a, c.dtype, kind == Tensor::kTile128, st);
   if (e == cudaSuccess) e = launch_attn_merge(a, g.ctas, g.rows, t.dtype, st);
   return e == cudaSuccess ? DROPKV_OK : cuda_fail(e);
 }

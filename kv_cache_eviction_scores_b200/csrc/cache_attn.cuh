@@ -224,8 +224,10 @@ struct AttnGrid {
 // Grid and unit rows of each kernel (host); launchers of one call's kernels.
 AttnGrid attn_grid_simt();
 AttnGrid attn_grid_rows();
+AttnGrid attn_grid_tile(bool alt);
 cudaError_t launch_attn_simt(const AttnDev& a, int page_dtype, int q_dtype, cudaStream_t st);
 cudaError_t launch_attn_rows(const AttnDev& a, int page_dtype, cudaStream_t st);
+cudaError_t launch_attn_tile(const AttnDev& a, int page_dtype, bool alt, cudaStream_t st);
 cudaError_t launch_attn_merge(const AttnDev& a, int ctas, int rows, int q_dtype, cudaStream_t st);
 
 }  // namespace dropkv

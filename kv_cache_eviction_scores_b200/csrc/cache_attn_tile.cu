@@ -1,0 +1,845 @@
+// cache_attn_tile.cu -- cache attention for many query rows per KV head (chunks
+// of a prompt, long drafts): bf16 queries, bf16 or e4m3 pages, head dim 64/128,
+// on tcgen05 with the accumulators in TMEM.
+//
+// Mathematics: the online softmax of the row kernel (reference maximum in
+// log2 units that moves only when a logit exceeds it by more than 8; fp32 P
+// summed into l, P rounded to nearest bf16 for P V), one query row per thread.
+// e4m3 pages are widened to bf16 with their scale as they are staged: a
+// 4-bit significand times a power of two is a bf16 exactly, wherever bf16 has
+// the exponent (a row whose scale is under 2^-119 holds nothing above 2^-110,
+// and rounds there).
+//
+// Layout: a unit of 256 rows is two query tiles of 128 rows against tiles of
+// 128 slots; a staged K/V tile serves both, so the staging (four producer
+// warps: page lookups, asynchronous 16-byte copies or, for e4m3, loads, the
+// widening and stores) is paid once per 256 rows.  Per query tile u: S_u = Q_u
+// K^T (M = N = 128) in TMEM columns 128 u, P_u over it (each half of P over the
+// half of S that it comes from), O_u at 256 + 128 u, all 512 columns.  One softmax warpgroup per query tile; while
+// one tile's softmax runs, the other tile's MMAs fill the tensor pipe.  P V of
+// a tile begins when the upper half of P is there.
+// kAlt (units of at most 128 rows): one query tile, and the two warpgroups take
+// the slot tiles in turn, each with its own S/P and O, joined at a unit's end.
+//
+// Every role walks the CTA's range by itself, so that staging runs on into the
+// next unit while the last one is finished.  A slot without a page and the
+// slots that no row of the unit sees are staged as zeros and hidden by a mask
+// bit each.  Slots that only some rows see can hold an infinity or a NaN, and
+// 0 * NaN must not reach the other rows: the producers stage such values as 0
+// and raise the unit's flag, and the rows that do see them add them at the end.
+//
+// Every wait on an mbarrier is bounded (2 s of %globaltimer); on expiry the
+// kernel records DROPKV_ERR_TIMEOUT, every role leaves, and TMEM is freed.
+#include "cache_attn.cuh"
+#include "tc_ptx.cuh"
+
+namespace dropkv {
+
+namespace {
+
+using namespace tc;
+
+constexpr int kTThreads = 416, kTTile = 128, kTCtas = 148;
+constexpr int kTProd = 4;                    // producer warps 8..11
+constexpr int kTMmaWarp = 12;
+constexpr uint64_t kTWaitNs = 2000000000ull;
+constexpr uint32_t kTColO = 256;
+
+template <int D, bool kAlt>
+struct TileShared {
+  static constexpr int kStages = kAlt ? 3 : 2;
+  static constexpr int kQTiles = kAlt ? 1 : 2;
+  static constexpr int kBox = 128 * 128;                   // 128 rows x 64 bf16, 128-byte swizzle
+  static constexpr int kTileBytes = D / 64 * kBox;
+  static constexpr int kBars = 2 + 4 * kStages + 10;
+  static constexpr int oK = kQTiles * kTileBytes;
+  static constexpr int oV = oK + kStages * kTileBytes;
+  static constexpr int oBars = oV + kStages * kTileBytes;
+  static constexpr int oMask = oBars + (kBars + 1) / 2 * 16;  // uint32 [8][4]
+  static constexpr int oOdd = oMask + 128;                    // int [2]
+  static constexpr int oMisc = oOdd + 16;                     // TMEM base, abort flag
+  static constexpr int oXml = oMisc + 16;                     // float2 [2][128], kAlt
+  static constexpr int oPlan = oXml + (kAlt ? 2 * 128 * 8 : 0);
+  static constexpr int kBytes = oPlan + (int)sizeof(AttnPlanShared);
+};
+
+__device__ __forceinline__ float f32(uint32_t u) { return __uint_as_float(u); }
+__device__ __forceinline__ uint32_t u32(float f) { return __float_as_uint(f); }
+
+__device__ __forceinline__ void fail(const AttnDev& a, volatile int* abort_flag) {
+  *abort_flag = 1;
+  if (a.status) atomicMax(a.status, (int)DROPKV_ERR_TIMEOUT);
+}
+// The outcome is the same for every lane, so the warp stays converged.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, kTWaitNs));
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
+  const int n = on ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void sts16(uint32_t dst, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t src) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(src)
+               : "memory");
+  return v;
+}
+
+// 64 consecutive 32-bit columns for every lane, in two loads with one wait.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
+#define DKV_O32(i) DKV_O8(i), DKV_O8(i + 8), DKV_O8(i + 16), DKV_O8(i + 24)
+#define DKV_O8(i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), \
+                  "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, "
+      "%8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, "
+      "%24, %25, %26, %27, %28, %29, %30, %31}, [%64];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32, %33, %34, %35, %36, %37, %38, %39, "
+      "%40, %41, %42, %43, %44, %45, %46, %47, "
+      "%48, %49, %50, %51, %52, %53, %54, %55, "
+      "%56, %57, %58, %59, %60, %61, %62, %63}, [%65];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : DKV_O32(0), DKV_O32(32)
+      : "r"(taddr), "r"(taddr + 32u)
+      : "memory");
+#undef DKV_O8
+#undef DKV_O32
+}
+// 16 bytes, or zeros when !on; volatile, so that it is issued here and not
+// where the value is used.
+__device__ __forceinline__ uint4 ldg16(const void* p, bool on) {
+  uint4 v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+      "@p ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(p), "r"((int)on));
+  return v;
+}
+__device__ __forceinline__ uint32_t ldg1(const uint8_t* p, bool on) {
+  uint32_t v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b32 %0, 0;\n\t"
+      "@p ld.global.nc.u8 %0, [%1];\n\t}"
+      : "=&r"(v)
+      : "l"(p), "r"((int)on));
+  return v;
+}
+
+// Byte offset of 16-byte piece c (eight bf16) of row r in a staged tile.
+__device__ __forceinline__ uint32_t piece_at(int r, int c) {
+  return (uint32_t)((c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+__device__ __forceinline__ bool non_finite(uint32_t two) {  // of a bf16 pair
+  return (two & 0x7F80u) == 0x7F80u || (two & 0x7F800000u) == 0x7F800000u;
+}
+__device__ __forceinline__ uint32_t without_non_finite(uint32_t two) {
+  if ((two & 0x7F80u) == 0x7F80u) two &= 0xFFFF0000u;
+  if ((two & 0x7F800000u) == 0x7F800000u) two &= 0x0000FFFFu;
+  return two;
+}
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// A row scale 2^(byte - 127) as the bf16 factors that take the bits of e4m3 on
+// their way to bf16 (the seven magnitude bits at the bottom of the exponent,
+// the value times 2^-120): 2^(byte - 7), and 2^127 at most, twice in x; the
+// rest, 1 but for bytes above 134, twice in y.  NaN for 255.
+__device__ __forceinline__ uint2 widen_factors(uint32_t byte) {
+  const uint32_t lo = byte == 255u ? 0x7FC0u : (min(byte, 134u) + 120u) << 7;
+  const uint32_t hi = byte == 255u || byte <= 134u ? 0x3F80u : (byte - 134u + 127u) << 7;
+  return make_uint2(lo * 0x10001u, hi * 0x10001u);
+}
+// Two e4m3 bytes in bits 15..8 and 31..24 of x, the rest 0, to a bf16 pair.
+__device__ __forceinline__ uint32_t widen2(uint32_t x, uint32_t f) {
+  return mul_bf16x2(((x >> 4) & 0x07F007F0u) | (x & 0x80008000u), f);
+}
+
+// The rows of one unit as a role sees them.
+struct Unit {
+  int b, rt, rows, seen_all, seen_min, L, n;
+};
+template <int kRows>
+__device__ __forceinline__ Unit unit_of(const AttnDev& a, const AttnWalk& w) {
+  Unit x;
+  x.b = w.item / a.nrt;
+  x.rt = w.item - x.b * a.nrt;
+  attn_lengths(a, x.b, x.L, x.n);
+  x.rows = min(kRows, a.G * x.n - x.rt * kRows);
+  x.seen_all = attn_seen(a, x.L, x.n, x.rt * kRows + x.rows - 1);
+  x.seen_min = attn_seen(a, x.L, x.n, x.rt * kRows);
+  return x;
+}
+
+// Pool row of slot `slot`, or -1 (32 bits: the host checked the pools' size).
+struct Look {
+  int page, off;  // page -2: a slot without a page; -1: no slot
+};
+__device__ __forceinline__ Look look_up(const AttnDev& a, int b, int slot, int end) {
+  Look k = {-1, 0};
+  if (slot < end) {
+    const int pi = (int)a.c.fpage.div((uint32_t)slot);
+    k.page = __ldg(a.c.table + (size_t)b * a.c.max_pages + pi);
+    k.off = slot - pi * a.c.page;
+    if (k.page == -1) k.page = -2;
+  }
+  return k;
+}
+__device__ __forceinline__ int pool_row(const AttnDev& a, int h, Look k) {
+  if ((uint32_t)k.page < (uint32_t)a.c.n_pages) return (k.page * a.c.Hkv + h) * a.c.page + k.off;
+  if (k.page != -1) raise_arg(a.status);
+  return -1;
+}
+
+// The infinities and NaNs of V that a row sees, of its unit's partly seen
+// slots: added to 32 columns of its O from column c0 on (rare).
+template <typename TP, int D>
+__device__ __forceinline__ void add_non_finite(const AttnDev& a, int b, int h, int j0, int j1, int c0,
+                                            uint32_t (&o)[32]) {
+#pragma unroll 1
+  for (int j = j0; j < j1; ++j) {
+    const int64_t row = cache_row(a.c, b, h, j);
+    if (row < 0) continue;
+    if (sizeof(TP) == 1) {
+      const uint32_t byte = a.c.vs[row];
+      const uint8_t* v = reinterpret_cast<const uint8_t*>(a.c.v) + row * D + c0;
+#pragma unroll
+      for (int x = 0; x < 32; ++x) {
+        const float y = unpack_e4m3(v[x]).x * scale_of(byte);
+        if (byte == 255u || isinf(y)) o[x] = u32(f32(o[x]) + y);
+      }
+    } else {
+      const uint16_t* v = reinterpret_cast<const uint16_t*>(a.c.v) + row * D + c0;
+#pragma unroll
+      for (int x = 0; x < 32; ++x)
+        if ((v[x] & 0x7F80u) == 0x7F80u) o[x] = u32(f32(o[x]) + f32((uint32_t)v[x] << 16));
+    }
+  }
+}
+
+template <typename TP, int D, bool kAlt>
+__global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
+  using S = TileShared<D, kAlt>;
+  constexpr int kStages = S::kStages, kRows = kAlt ? 128 : 256;
+  constexpr bool kScaled = sizeof(TP) == 1;
+  constexpr int kPieces = D / 8;  // of a staged row
+  extern __shared__ __align__(1024) uint8_t sm[];
+  pdl_trigger();
+  const uint32_t base = smem_u32(sm);
+  if (base & 1023u) {  // the swizzled tiles need 1 KB alignment
+    if (threadIdx.x == 0) {
+      a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+      if (a.status) atomicMax(a.status, (int)DROPKV_ERR_CUDA);
+    }
+    return;
+  }
+  AttnPlanShared& plan = *reinterpret_cast<AttnPlanShared*>(sm + S::oPlan);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + S::oMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + S::oMisc + 4);
+  volatile uint32_t* smask = reinterpret_cast<volatile uint32_t*>(sm + S::oMask);
+  volatile int* sodd = reinterpret_cast<volatile int*>(sm + S::oOdd);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto bar = [&](int i) { return base + S::oBars + 8 * i; };
+  // Q full / empty; K and V full / empty per stage; per query tile (or, kAlt,
+  // warpgroup): S there, P's upper and lower half there, P V done
+  const uint32_t QF = bar(0), QE = bar(1);
+  auto KF = [&](int s) { return bar(2 + s); };
+  auto KE = [&](int s) { return bar(2 + kStages + s); };
+  auto VF = [&](int s) { return bar(2 + 2 * kStages + s); };
+  auto VE = [&](int s) { return bar(2 + 3 * kStages + s); };
+  constexpr int kB0 = 2 + 4 * kStages;
+  auto SF = [&](int u) { return bar(kB0 + u); };
+  auto PA = [&](int u) { return bar(kB0 + 2 + u); };
+  auto PB = [&](int u) { return bar(kB0 + 4 + u); };
+  auto PD = [&](int u) { return bar(kB0 + 6 + u); };
+  // units of even / odd number finished by the softmax warps
+  auto UE = [&](int p) { return bar(kB0 + 8 + p); };
+  if (threadIdx.x == 0) {
+    mbar_init(QF, kTProd);
+    mbar_init(QE, 1);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(KF(s), kTProd);
+      mbar_init(KE(s), 1);
+      mbar_init(VF(s), kTProd);
+      mbar_init(VE(s), 1);
+    }
+    for (int u = 0; u < 2; ++u) {
+      mbar_init(SF(u), 1);
+      mbar_init(PA(u), 4);
+      mbar_init(PB(u), 4);
+      mbar_init(PD(u), 1);
+      mbar_init(UE(u), 8);
+      sodd[u] = 0;
+    }
+    *abort_flag = 0;
+    a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    fence_mbar_init();
+  }
+  if (warp == kTMmaWarp) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  int64_t total;
+  int grid;
+  AttnWalk w;
+  bool more = attn_plan<kRows, kTTile, kTThreads>(a, plan, w, total, grid);
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_slot;
+
+  if (warp >= kTMmaWarp) {
+    if (warp == kTMmaWarp) {
+      // ---------------- MMA issuer ----------------
+      constexpr uint32_t IDS = idesc_bf16(128, 128, false, false);  // S = Q K^T
+      constexpr uint32_t IDP = idesc_bf16(128, D, false, true);     // O += P V (V MN-major)
+      const SDesc qd = sdesc_split(base, 16, 1024);
+      const SDesc kd = sdesc_split(base + S::oK, 16, 1024);
+      const SDesc vd = sdesc_split(base + S::oV, S::kBox, 1024);
+      uint32_t kc = 0, vc = 0;             // slot tiles whose S / P V are all issued
+      uint32_t ns[2] = {0, 0}, np[2] = {0, 0};  // S and P V issued per warpgroup
+      uint32_t units = 0;
+      bool ok = true;
+      // S = Q_q K^T of the kc-th tile into warpgroup u's columns, once the P V
+      // that reads its last P from there is done
+      auto issue_S = [&](int u, int q, bool last_of_tile, bool last_of_unit) {
+        const uint32_t s = kc % kStages;
+        if (!warp_wait(KF(s), (kc / kStages) & 1)) return false;
+        if (ns[u] >= 1 && !warp_wait(PD(u), (ns[u] - 1) & 1)) return false;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t qlo = qd.lo + (uint32_t)q * (S::kTileBytes >> 4);
+          const uint32_t klo = kd.lo + s * (S::kTileBytes >> 4);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t at = (uint32_t)((kk >> 2) * (S::kBox >> 4) + (kk & 3) * 2);
+            mma_ss_w(tbase + 128u * u, qlo + at, qd.hi, klo + at, kd.hi, IDS, kk > 0 ? 1u : 0u);
+          }
+          mma_commit(SF(u));
+          if (last_of_tile) mma_commit(KE(s));
+          if (last_of_unit) mma_commit(QE);
+        }
+        __syncwarp();
+        ++ns[u];
+        if (last_of_tile) ++kc;
+        return true;
+      };
+      // O_u (+)= P_u V of the vc-th tile
+      auto issue_PV = [&](int u, bool first, bool last_of_tile) {
+        const uint32_t s = vc % kStages;
+        if (!warp_wait(VF(s), (vc / kStages) & 1)) return false;
+        const uint32_t vlo = vd.lo + s * (S::kTileBytes >> 4);
+        const uint32_t dO = tbase + kTColO + 128u * u, pS = tbase + 128u * u;
+#pragma unroll
+        for (int half = 1; half >= 0; --half) {
+          if (!warp_wait(half ? PA(u) : PB(u), np[u] & 1)) return false;
+          tc_fence_after();
+          if (lane == 0) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)  // V slices of 16 rows, 2 KB
+              mma_ts_w(dO, pS + 64u * half + 8u * kk, vlo + 128u * (4 * half + kk), vd.hi, IDP,
+                       (!first || half == 0 || kk > 0) ? 1u : 0u);
+          }
+        }
+        if (lane == 0) {
+          mma_commit(PD(u));
+          if (last_of_tile) mma_commit(VE(s));
+        }
+        __syncwarp();
+        ++np[u];
+        if (last_of_tile) ++vc;
+        return true;
+      };
+      while (more && ok) {
+        const Unit x = unit_of<kRows>(a, w);
+        const int T = w.t1 - w.t0;
+        ok = warp_wait(QF, units & 1);
+        ++units;
+        tc_fence_after();
+        if (kAlt) {
+          for (int j = 0; j < 2 && j < T && ok; ++j) ok = issue_S(j, 0, true, j == T - 1);
+          for (int j = 0; j < T && ok; ++j) {
+            ok = issue_PV(j & 1, j < 2, true);
+            if (ok && j + 2 < T) ok = issue_S(j & 1, 0, true, j + 2 == T - 1);
+          }
+        } else {
+          const int nt = x.rows > 128 ? 2 : 1;
+          for (int u = 0; u < nt && ok; ++u) ok = issue_S(u, u, u == nt - 1, T == 1 && u == nt - 1);
+          for (int j = 0; j < T && ok; ++j)
+            for (int u = 0; u < nt && ok; ++u) {
+              ok = issue_PV(u, j == 0, u == nt - 1);
+              if (ok && j + 1 < T)
+                ok = issue_S(u, u, u == nt - 1, j + 1 == T - 1 && u == nt - 1);
+            }
+        }
+        if (!ok) {
+          if (lane == 0) fail(a, abort_flag);
+          break;
+        }
+        more = attn_next<kRows, kTTile>(a, w);
+      }
+    }
+  } else if (warp >= 8) {
+    // ---------------- producers ----------------
+    // Warp pw stages the slots 32 pw .. 32 pw + 31 of every tile, and the
+    // query rows 32 pw ..; lane i looks up slot i.
+    const int pw = warp - 8;
+    uint32_t tc_ = 0, units = 0;  // tiles and units so far
+    bool ok = true;
+    const uint8_t* kp = reinterpret_cast<const uint8_t*>(a.c.k);
+    const uint8_t* vp = reinterpret_cast<const uint8_t*>(a.c.v);
+    auto arrive = [&](uint32_t b) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b);
+    };
+    auto load_q = [&](const Unit& x) {
+      // the unit's query rows, zeros behind the last
+      constexpr int kPer = 32 / kPieces;  // rows a warp copies at once
+      const int c = lane % kPieces;
+      for (int q = 0; q < S::kQTiles; ++q) {
+#pragma unroll 4
+        for (int i = 0; i < 32 / kPer; ++i) {
+          const int r = pw * 32 + i * kPer + lane / kPieces, ur = q * 128 + r;
+          const bool on = ur < x.rows;
+          const AttnRow y = attn_row(a, x.b, w.h, x.rt * kRows + (on ? ur : 0));
+          const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(a.q) + y.b * a.qs[0] +
+                                     y.hq * a.qs[1] + y.t * a.qs[2] + c * 8;
+          copy16(base + q * S::kTileBytes + piece_at(r, c), src, on);
+        }
+      }
+      copy_commit();
+    };
+    while (more && ok) {
+      // at most one unit ahead of the softmax warps: they read sodd at a unit's end
+      ok = units < 2 || warp_wait(UE(units & 1), ((units >> 1) - 1) & 1);
+      if (!ok) break;
+      const Unit x = unit_of<kRows>(a, w);
+      // lane's slot of tile t, and the word of the tile's slots that are there
+      auto look = [&](int t) {
+        return look_up(a, x.b, t < w.t1 ? t * kTTile + pw * 32 + lane : x.seen_all, x.seen_all);
+      };
+      auto odd = [&]() { sodd[units & 1] = (int)units + 1; };
+      Look nxt = look(w.t0);
+      if constexpr (!kScaled) {
+        constexpr int kPer = 32 / kPieces;
+        const int c = lane % kPieces;
+        // non-finite values of partly seen slots of V, as they landed in stage s
+        auto clean = [&](int t, uint32_t s) {
+          if ((t + 1) * kTTile <= x.seen_min) return;
+          bool any = false;
+          for (int i = 0; i < 32 / kPer; ++i) {
+            const int r = pw * 32 + i * kPer + lane / kPieces;
+            if (t * kTTile + r < x.seen_min) continue;
+            const uint32_t at = base + S::oV + s * S::kTileBytes + piece_at(r, c);
+            uint4 v = lds16(at);
+            if (non_finite(v.x) || non_finite(v.y) || non_finite(v.z) || non_finite(v.w)) {
+              any = true;
+              sts16(at, make_uint4(without_non_finite(v.x), without_non_finite(v.y),
+                                   without_non_finite(v.z), without_non_finite(v.w)));
+            }
+          }
+          if (any) odd();
+        };
+        for (int t = w.t0; t < w.t1 && ok; ++t) {
+          const int row = pool_row(a, w.h, nxt);
+          nxt = look(t + 1);
+          const uint32_t s = tc_ % kStages, ph = (tc_ / kStages) & 1;
+          const uint32_t word = __ballot_sync(0xffffffffu, row >= 0);
+          // K of this tile, then the last tile's V is handed over; V, then K
+          ok = warp_wait(KE(s), ph ^ 1);
+          if (!ok) break;
+          if (lane == 0) smask[(tc_ & 7) * 4 + pw] = word;
+          auto issue = [&](const uint8_t* pool, uint32_t dst) {
+#pragma unroll 8
+            for (int i = 0; i < 32 / kPer; ++i) {
+              const int at = __shfl_sync(0xffffffffu, row, i * kPer + lane / kPieces);
+              copy16(dst + piece_at(pw * 32 + i * kPer + lane / kPieces, c),
+                     pool + (at < 0 ? 0 : (size_t)at * (D * 2) + c * 16), at >= 0);
+            }
+            copy_commit();
+          };
+          issue(kp, base + S::oK + s * S::kTileBytes);
+          if (t == w.t0) {
+            // the last unit's rows are read out: this one's
+            ok = warp_wait(QE, (units & 1) ^ 1);
+            if (!ok) break;
+            load_q(x);
+            copy_wait<0>();
+            arrive(QF);
+            arrive(KF(s));
+          } else {
+            copy_wait<1>();
+            const uint32_t sl = (tc_ - 1) % kStages;
+            clean(t - 1, sl);
+            arrive(VF(sl));
+          }
+          ok = warp_wait(VE(s), ph ^ 1);
+          if (!ok) break;
+          issue(vp, base + S::oV + s * S::kTileBytes);
+          if (t != w.t0) {
+            copy_wait<1>();
+            arrive(KF(s));
+          }
+          ++tc_;
+        }
+        copy_wait<0>();
+        if (ok) {
+          const uint32_t sl = (tc_ - 1) % kStages;
+          clean(w.t1 - 1, sl);
+          arrive(VF(sl));
+        }
+      } else {
+        // a row of D bytes is D / 16 loads; a warp's pass covers kPer rows
+        constexpr int kIn = D / 16, kPer = 32 / kIn, kPass = 32 / kPer;
+        const int c = lane % kIn;
+        uint4 rk[kPass], rv[kPass];
+        uint32_t bk, bv;  // scale bytes of the lane's slot
+        auto load = [&](const uint8_t* pool, int row, uint4 (&to)[kPass]) {
+#pragma unroll
+          for (int i = 0; i < kPass; ++i) {
+            const int at = __shfl_sync(0xffffffffu, row, i * kPer + lane / kIn);
+            to[i] = ldg16(pool + (size_t)max(at, 0) * D + c * 16, at >= 0);
+          }
+        };
+        // widened into a stage; values of partly seen slots (from row `part` of
+        // the tile on) that are not finite as 0
+        auto store = [&](const uint4 (&from)[kPass], uint32_t byte, uint32_t dst, int part) {
+          bool any = false;
+#pragma unroll
+          for (int i = 0; i < kPass; ++i) {
+            const int r = i * kPer + lane / kIn;
+            const uint2 f = widen_factors(__shfl_sync(0xffffffffu, byte, r));
+            const uint32_t in[4] = {from[i].x, from[i].y, from[i].z, from[i].w};
+            uint32_t y[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              y[2 * k] = widen2(__byte_perm(in[k], 0, 0x1404), f.x);
+              y[2 * k + 1] = widen2(__byte_perm(in[k], 0, 0x3424), f.x);
+            }
+            if (f.y != 0x3F803F80u) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) y[k] = mul_bf16x2(y[k], f.y);
+            }
+            if (pw * 32 + r >= part) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                any = any || non_finite(y[k]);
+                y[k] = without_non_finite(y[k]);
+              }
+            }
+            // lanes of the second box store their odd piece first: eight lanes of a
+            // row then hit eight different 16-byte bank groups
+            const bool swap = D == 128 && c >= kIn / 2;
+            const uint4 p0 = make_uint4(y[0], y[1], y[2], y[3]), p1 = make_uint4(y[4], y[5], y[6], y[7]);
+            sts16(dst + piece_at(pw * 32 + r, 2 * c + swap), swap ? p1 : p0);
+            sts16(dst + piece_at(pw * 32 + r, 2 * c + !swap), swap ? p0 : p1);
+          }
+          if (any) odd();
+        };
+        int row = pool_row(a, w.h, nxt);
+        nxt = look(w.t0 + 1);
+        load(kp, row, rk);
+        load(vp, row, rv);
+        bk = ldg1(a.c.ks + max(row, 0), row >= 0);
+        bv = ldg1(a.c.vs + max(row, 0), row >= 0);
+        for (int t = w.t0; t < w.t1 && ok; ++t) {
+          const uint32_t s = tc_ % kStages, ph = (tc_ / kStages) & 1;
+          const uint32_t word = __ballot_sync(0xffffffffu, row >= 0);
+          row = pool_row(a, w.h, nxt);
+          nxt = look(t + 2);
+          ok = warp_wait(KE(s), ph ^ 1);
+          if (!ok) break;
+          if (lane == 0) smask[(tc_ & 7) * 4 + pw] = word;
+          store(rk, bk, base + S::oK + s * S::kTileBytes, kTTile);
+          arrive(KF(s));
+          load(kp, row, rk);
+          bk = ldg1(a.c.ks + max(row, 0), row >= 0);
+          if (t == w.t0) {
+            ok = warp_wait(QE, (units & 1) ^ 1);
+            if (!ok) break;
+            load_q(x);
+            copy_wait<0>();
+            arrive(QF);
+          }
+          ok = warp_wait(VE(s), ph ^ 1);
+          if (!ok) break;
+          store(rv, bv, base + S::oV + s * S::kTileBytes, x.seen_min - t * kTTile);
+          arrive(VF(s));
+          load(vp, row, rv);
+          bv = ldg1(a.c.vs + max(row, 0), row >= 0);
+          ++tc_;
+        }
+      }
+      if (!ok) break;
+      ++units;
+      more = attn_next<kRows, kTTile>(a, w);
+    }
+    if (!ok && lane == 0) fail(a, abort_flag);
+    copy_wait<0>();
+  } else {
+    // ---------------- softmax ----------------
+    const int u = warp >> 2, ql = warp & 3;
+    const int row = ql * 32 + lane;                  // row of the query tile
+    const int crow = kAlt ? row : 128 * u + row;     // row of the unit
+    const uint32_t lane_off = (uint32_t)(ql * 32) << 16;
+    const uint32_t tS = tbase + 128u * u + lane_off;
+    const uint32_t tO = tbase + kTColO + 128u * u + lane_off;
+    const float c = a.c_log2;
+    const uint64_t c2 = pk2(c, c);
+    uint32_t n = 0;              // slot tiles of this warpgroup so far
+    uint32_t other = 0;          // kAlt: of the other one
+    uint32_t tiles = 0, units = 0;
+    bool live = true;            // no wait has run out
+    auto alive = [&](bool got) {
+      if (!got || __any_sync(0xffffffffu, *abort_flag != 0)) {
+        if (!got && lane == 0) fail(a, abort_flag);
+        live = false;
+      }
+    };
+    while (more) {
+      const Unit x = unit_of<kRows>(a, w);
+      const int T = w.t1 - w.t0;
+      const bool warp_rows = (kAlt ? 0 : 128 * u) + ql * 32 < x.rows;
+      const bool has = crow < x.rows;
+      const int r = x.rt * kRows + crow;
+      const int seen = has ? attn_seen(a, x.L, x.n, r) : 0;
+      float m = -CUDART_INF_F, l = 0.f;
+      const bool mine = kAlt || 128 * u < x.rows;  // this query tile exists
+      for (int j = kAlt ? u : 0; j < T && live && mine; j += kAlt ? 2 : 1) {
+        alive(warp_wait(SF(u), n & 1));
+        if (!live) break;
+        if (warp_rows) {
+          tc_fence_after();
+          uint32_t sr[64];
+          const int tok0 = (w.t0 + j) * kTTile, lim = seen - tok0;
+          const volatile uint32_t* mw = smask + ((tiles + j) & 7) * 4;
+          const bool masked = tok0 + kTTile > x.seen_min || (mw[0] & mw[1] & mw[2] & mw[3]) != ~0u;
+          auto load_half = [&](int half) {
+            tmem_ld64(tS + 64u * half, sr);
+            if (masked) {
+              const uint32_t wa = mw[2 * half], wb = mw[2 * half + 1];
+#pragma unroll
+              for (int k = 0; k < 64; ++k)
+                if (64 * half + k >= lim || !(((k < 32 ? wa : wb) >> (k & 31)) & 1)) sr[k] = 0xFF800000u;
+            }
+          };
+          float ya = -CUDART_INF_F, yb = -CUDART_INF_F;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            load_half(half);
+#pragma unroll
+            for (int k = 0; k < 64; k += 4) {
+              ya = fmax3(ya, f32(sr[k]), f32(sr[k + 1]));
+              yb = fmax3(yb, f32(sr[k + 2]), f32(sr[k + 3]));
+            }
+          }
+          const float mt = fmaxf(ya, yb) * c;  // c > 0
+          float fac = 1.f;
+          if (mt > m + 8.f) {
+            fac = m == -CUDART_INF_F ? 0.f : attn_ex2(m - mt);
+            m = mt;
+            l *= fac;
+          }
+          // rows whose reference moved: O, complete up to the last tile, by fac
+          if (__any_sync(0xffffffffu, fac != 1.f) && j >= (kAlt ? 2 : 1)) {
+            if (!warp_wait(PD(u), (n - 1) & 1)) {
+              alive(false);
+              break;
+            }
+            tc_fence_after();
+#pragma unroll 1
+            for (int k = 0; k < D / 16; ++k) {
+              uint32_t o[16];
+              tmem_ld16(tO + 16u * k, o);
+#pragma unroll
+              for (int y = 0; y < 16; ++y) o[y] = u32(f32(o[y]) * fac);
+              tmem_st16(tO + 16u * k, o);
+            }
+            tmem_st_wait();
+          }
+          const float mu = m == -CUDART_INF_F ? 0.f : m;
+          const uint64_t nmu2 = pk2(-mu, -mu);
+          uint64_t l2 = pk2(l, 0.f);
+#pragma unroll
+          for (int half = 1; half >= 0; --half) {  // the upper half is in registers
+            if (half == 0) load_half(0);
+            uint32_t pw[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              float d0, d1;
+              upk2(ffma2(pk2(f32(sr[2 * k]), f32(sr[2 * k + 1])), c2, nmu2), d0, d1);
+              const float e0 = attn_ex2(d0), e1 = attn_ex2(d1);
+              l2 = fadd2(l2, pk2(e0, e1));
+              pw[k] = pack_bf16(e0, e1);
+            }
+            tmem_st32(tS + 64u * half, pw);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(half ? PA(u) : PB(u));
+          }
+          float la, lb;
+          upk2(l2, la, lb);
+          l = la + lb;
+        } else {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(PA(u));
+            mbar_arrive(PB(u));
+          }
+        }
+        ++n;
+      }
+      // ---- the unit's rows: O / l, or the cut unit's partial ----
+      const int slot = attn_slot(w);
+      const AttnRow at = attn_row(a, x.b, w.h, has ? r : x.rt * kRows);
+      __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) + at.b * a.os[0] +
+                           at.hq * a.os[1] + at.t * a.os[2];
+      float* part = a.part + ((size_t)(slot < 0 ? 0 : slot) * kRows + crow) * a.pstride;
+      const int j0 = max(w.t0 * kTTile, x.seen_min), j1 = min(w.t1 * kTTile, seen);
+      auto finish = [&](uint32_t (&o)[32], int c0, bool fix, float inv) {
+        if (fix) add_non_finite<TP, D>(a, x.b, w.h, j0, j1, c0, o);
+        if (!has) return;
+        if (slot < 0) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 8) {
+            uint32_t y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              y[e] = pack_bf16(f32(o[k + 2 * e]) * inv, f32(o[k + 2 * e + 1]) * inv);
+            *reinterpret_cast<uint4*>(out + c0 + k) = make_uint4(y[0], y[1], y[2], y[3]);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; k += 4)
+            *reinterpret_cast<float4*>(part + c0 + k) =
+                make_float4(f32(o[k]), f32(o[k + 1]), f32(o[k + 2]), f32(o[k + 3]));
+        }
+      };
+      auto put_stats = [&](float mm, float ll) {
+        if (!has) return;
+        if (slot < 0)
+          attn_put_lse(a, at, mm, ll);
+        else
+          *reinterpret_cast<float2*>(part + a.pstride - 4) = make_float2(mm, ll);
+      };
+      if constexpr (!kAlt) {
+        if (mine && live) alive(warp_wait(PD(u), (n - 1) & 1));
+        if (mine && live && warp_rows) {
+          tc_fence_after();
+          const bool fix = sodd[units & 1] == (int)units + 1;
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+          for (int k = 0; k < D / 32; ++k) {
+            uint32_t o[32];
+            tmem_ld32(tO + 32u * k, o);
+            finish(o, 32 * k, fix, inv);
+          }
+          put_stats(m, l);
+        }
+        tc_fence_before();
+      } else {
+        // both warpgroups' rows, each half of the columns
+        float2* xml = reinterpret_cast<float2*>(sm + S::oXml);
+        other += u == 0 ? (uint32_t)(T / 2) : (uint32_t)((T + 1) / 2);
+        if (live && n > 0) alive(warp_wait(PD(u), (n - 1) & 1));
+        if (live && other > 0) alive(warp_wait(PD(u ^ 1), (other - 1) & 1));
+        xml[u * 128 + row] = make_float2(m, l);
+        named_barrier_sync(1, 256);
+        tc_fence_after();
+        if (live && warp_rows) {
+          const float2 a0 = xml[row], a1 = xml[128 + row];
+          const float M = fmaxf(a0.x, a1.x);
+          auto weight = [&](float2 y) {
+            return y.x == -CUDART_INF_F ? (y.y == 0.f ? 0.f : y.y) : attn_ex2(y.x - M);
+          };
+          const float f0 = weight(a0), f1 = weight(a1);
+          auto part_of = [&](float2 y, float f) { return y.x == -CUDART_INF_F ? y.y : y.y * f; };
+          const float ll = part_of(a0, f0) + part_of(a1, f1);
+          const bool fix = sodd[units & 1] == (int)units + 1;
+          const float inv = ll == 0.f ? 0.f : 1.f / ll;
+          const uint32_t t0 = tbase + kTColO + lane_off;
+#pragma unroll 1
+          for (int k = u * (D / 64); k < (u + 1) * (D / 64); ++k) {
+            uint32_t o[32];
+            tmem_ld32(t0 + 32u * k, o);
+#pragma unroll
+            for (int y = 0; y < 32; ++y) o[y] = u32(f32(o[y]) * f0);
+            if (T > 1) {
+              uint32_t o1[32];
+              tmem_ld32(t0 + 128u + 32u * k, o1);
+#pragma unroll
+              for (int y = 0; y < 32; ++y) o[y] = u32(fmaf(f32(o1[y]), f1, f32(o[y])));
+            }
+            finish(o, 32 * k, fix, inv);
+          }
+          if (u == 0) put_stats(M, ll);
+        }
+        tc_fence_before();
+        named_barrier_sync(1, 256);  // O and xml are read out
+      }
+      if (slot >= 0 && (slot & 1) && threadIdx.x == 0) attn_describe(a, w, total, grid);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(UE(units & 1));
+      tiles += T;
+      ++units;
+      more = attn_next<kRows, kTTile>(a, w);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kTMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+template <typename TP, int D, bool kAlt>
+cudaError_t launch_tile(const AttnDev& a, cudaStream_t st) {
+  const auto kern = k_attn_tile<TP, D, kAlt>;
+  constexpr int smem = TileShared<D, kAlt>::kBytes;
+  static_assert(smem <= 232448, "shared memory of a CTA");
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<kTCtas, kTThreads, smem, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <bool kAlt>
+cudaError_t launch_tiles(const AttnDev& a, int page_dtype, cudaStream_t st) {
+  if (page_dtype == DROPKV_BF16)
+    return a.c.d == 128 ? launch_tile<__nv_bfloat16, 128, kAlt>(a, st)
+                        : launch_tile<__nv_bfloat16, 64, kAlt>(a, st);
+  return a.c.d == 128 ? launch_tile<E4M3, 128, kAlt>(a, st) : launch_tile<E4M3, 64, kAlt>(a, st);
+}
+
+}  // namespace
+
+AttnGrid attn_grid_tile(bool alt) { return {kTCtas, alt ? 128 : 256}; }
+
+cudaError_t launch_attn_tile(const AttnDev& a, int page_dtype, bool alt, cudaStream_t st) {
+  return alt ? launch_tiles<true>(a, page_dtype, st) : launch_tiles<false>(a, page_dtype, st);
+}
+
+}  // namespace dropkv
