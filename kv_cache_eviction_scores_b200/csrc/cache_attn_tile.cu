@@ -160,18 +160,22 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// A row scale 2^(byte - 127) as the bf16 factors that take the bits of e4m3 on
-// their way to bf16 (the seven magnitude bits at the bottom of the exponent,
-// the value times 2^-120): 2^(byte - 7), and 2^127 at most, twice in x; the
-// rest, 1 but for bytes above 134, twice in y.  NaN for 255.
-__device__ __forceinline__ uint2 widen_factors(uint32_t byte) {
-  const uint32_t lo = byte == 255u ? 0x7FC0u : (min(byte, 134u) + 120u) << 7;
-  const uint32_t hi = byte == 255u || byte <= 134u ? 0x3F80u : (byte - 134u + 127u) << 7;
-  return make_uint2(lo * 0x10001u, hi * 0x10001u);
+// A row scale 2^(byte - 127) as two bf16 factors for the bits of e4m3 on their
+// way to bf16 (the seven magnitude bits at the bottom of the exponent: the value
+// times 2^-120): 2^(byte - 7), 2^127 at most, in the lower half; the rest, 1 but
+// for bytes above 134, in the upper.  NaN for 255.
+__device__ __forceinline__ uint32_t widen_factors(uint32_t byte) {
+  if (byte == 255u) return 0x3F807FC0u;
+  return ((min(byte, 134u) + 120u) << 7) | (byte <= 134u ? 0x3F80u : (byte - 134u + 127u) << 7) << 16;
 }
-// Two e4m3 bytes in bits 15..8 and 31..24 of x, the rest 0, to a bf16 pair.
+// Two e4m3 bytes of x to a bf16 pair, times f: the bytes, sign-extended to 16
+// bits each (kSel: byte i and its sign, byte j and its sign), four bits up, less
+// the copies of the sign between sign and exponent.
+template <uint32_t kSel>
 __device__ __forceinline__ uint32_t widen2(uint32_t x, uint32_t f) {
-  return mul_bf16x2(((x >> 4) & 0x07F007F0u) | (x & 0x80008000u), f);
+  uint32_t z;
+  asm("prmt.b32 %0, %1, %1, %2;" : "=r"(z) : "r"(x), "n"(kSel));
+  return mul_bf16x2((z << 4) & 0x87F087F0u, f);
 }
 
 // The rows of one unit as a role sees them.
@@ -192,21 +196,22 @@ __device__ __forceinline__ Unit unit_of(const AttnDev& a, const AttnWalk& w) {
 
 // Pool row of slot `slot`, or -1 (32 bits: the host checked the pools' size).
 struct Look {
-  int page, off;  // page -2: a slot without a page; -1: no slot
+  int page, off;  // off -1: no slot
 };
 __device__ __forceinline__ Look look_up(const AttnDev& a, int b, int slot, int end) {
-  Look k = {-1, 0};
+  Look k = {-1, -1};
   if (slot < end) {
     const int pi = (int)a.c.fpage.div((uint32_t)slot);
-    k.page = __ldg(a.c.table + (size_t)b * a.c.max_pages + pi);
+    // volatile: requested here, a tile before it is used
+    asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(k.page)
+                 : "l"(a.c.table + (size_t)b * a.c.max_pages + pi));
     k.off = slot - pi * a.c.page;
-    if (k.page == -1) k.page = -2;
   }
   return k;
 }
 __device__ __forceinline__ int pool_row(const AttnDev& a, int h, Look k) {
   if ((uint32_t)k.page < (uint32_t)a.c.n_pages) return (k.page * a.c.Hkv + h) * a.c.page + k.off;
-  if (k.page != -1) raise_arg(a.status);
+  if (k.off >= 0) raise_arg(a.status);
   return -1;
 }
 
@@ -470,7 +475,7 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
           if (!ok) break;
           if (lane == 0) smask[(tc_ & 7) * 4 + pw] = word;
           auto issue = [&](const uint8_t* pool, uint32_t dst) {
-#pragma unroll 8
+#pragma unroll 4
             for (int i = 0; i < 32 / kPer; ++i) {
               const int at = __shfl_sync(0xffffffffu, row, i * kPer + lane / kPieces);
               copy16(dst + piece_at(pw * 32 + i * kPer + lane / kPieces, c),
@@ -512,82 +517,106 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
         // a row of D bytes is D / 16 loads; a warp's pass covers kPer rows
         constexpr int kIn = D / 16, kPer = 32 / kIn, kPass = 32 / kPer;
         const int c = lane % kIn;
-        uint4 rk[kPass], rv[kPass];
-        uint32_t bk, bv;  // scale bytes of the lane's slot
-        auto load = [&](const uint8_t* pool, int row, uint4 (&to)[kPass]) {
+        // Jobs: K and V of a tile in turn, by the same code (one copy of it: see
+        // the softmax's loops); the next job's bytes are in flight.
+        uint4 now[kPass], nxt_[kPass];
+        auto load = [&](int v, int row, uint32_t& byte) {
+          const uint8_t* pool = v ? vp : kp;
 #pragma unroll
           for (int i = 0; i < kPass; ++i) {
             const int at = __shfl_sync(0xffffffffu, row, i * kPer + lane / kIn);
-            to[i] = ldg16(pool + (size_t)max(at, 0) * D + c * 16, at >= 0);
+            nxt_[i] = ldg16(pool + (size_t)max(at, 0) * D + c * 16, at >= 0);
+          }
+          byte = ldg1((v ? a.c.vs : a.c.ks) + max(row, 0), row >= 0);
+        };
+        // widened into a stage
+        auto put = [&](const uint32_t (&y)[8], int i, uint32_t dst) {
+          // lanes of the second box store their odd piece first: eight lanes of a
+          // row then hit eight different 16-byte bank groups
+          const int r = pw * 32 + i * kPer + lane / kIn;
+          const bool swap = D == 128 && c >= kIn / 2;
+          const uint4 p0 = make_uint4(y[0], y[1], y[2], y[3]), p1 = make_uint4(y[4], y[5], y[6], y[7]);
+          sts16(dst + piece_at(r, 2 * c + swap), swap ? p1 : p0);
+          sts16(dst + piece_at(r, 2 * c + !swap), swap ? p0 : p1);
+        };
+        auto widen = [&](const uint4& v, uint32_t f, uint32_t (&y)[8]) {
+          const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+          const uint32_t f2 = __byte_perm(f, 0, 0x1010);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            y[2 * k] = widen2<0x9180>(in[k], f2);
+            y[2 * k + 1] = widen2<0xB3A2>(in[k], f2);
           }
         };
-        // widened into a stage; values of partly seen slots (from row `part` of
-        // the tile on) that are not finite as 0
-        auto store = [&](const uint4 (&from)[kPass], uint32_t byte, uint32_t dst, int part) {
-          bool any = false;
+        auto store = [&](uint32_t byte, uint32_t dst, int part) {
+          const uint32_t own = widen_factors(byte);
 #pragma unroll
           for (int i = 0; i < kPass; ++i) {
-            const int r = i * kPer + lane / kIn;
-            const uint2 f = widen_factors(__shfl_sync(0xffffffffu, byte, r));
-            const uint32_t in[4] = {from[i].x, from[i].y, from[i].z, from[i].w};
             uint32_t y[8];
+            widen(now[i], __shfl_sync(0xffffffffu, own, i * kPer + lane / kIn), y);
+            put(y, i, dst);
+          }
+          if (part >= kTTile && __all_sync(0xffffffffu, own >> 16 == 0x3F80u)) return;
+          // large scales, or partly seen slots (from row `part` of the tile on),
+          // whose values that are not finite are staged as 0
+          bool any = false;
+#pragma unroll 1
+          for (int i = 0; i < kPass; ++i) {
+            const int r = pw * 32 + i * kPer + lane / kIn;
+            const uint32_t f = __byte_perm(__shfl_sync(0xffffffffu, own, r & 31), 0, 0x3232);
+#pragma unroll 1
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t at = dst + piece_at(r, 2 * c + e);
+              const uint4 v = lds16(at);
+              uint32_t y[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              y[2 * k] = widen2(__byte_perm(in[k], 0, 0x1404), f.x);
-              y[2 * k + 1] = widen2(__byte_perm(in[k], 0, 0x3424), f.x);
-            }
-            if (f.y != 0x3F803F80u) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k) y[k] = mul_bf16x2(y[k], f.y);
-            }
-            if (pw * 32 + r >= part) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                any = any || non_finite(y[k]);
-                y[k] = without_non_finite(y[k]);
+              for (int k = 0; k < 4; ++k) {
+                y[k] = mul_bf16x2(y[k], f);
+                any = any || (r >= part && non_finite(y[k]));
+                if (r >= part) y[k] = without_non_finite(y[k]);
               }
+              sts16(at, make_uint4(y[0], y[1], y[2], y[3]));
             }
-            // lanes of the second box store their odd piece first: eight lanes of a
-            // row then hit eight different 16-byte bank groups
-            const bool swap = D == 128 && c >= kIn / 2;
-            const uint4 p0 = make_uint4(y[0], y[1], y[2], y[3]), p1 = make_uint4(y[4], y[5], y[6], y[7]);
-            sts16(dst + piece_at(pw * 32 + r, 2 * c + swap), swap ? p1 : p0);
-            sts16(dst + piece_at(pw * 32 + r, 2 * c + !swap), swap ? p0 : p1);
           }
           if (any) odd();
         };
+        auto shift = [&]() {
+#pragma unroll
+          for (int i = 0; i < kPass; ++i) now[i] = nxt_[i];
+        };
         int row = pool_row(a, w.h, nxt);
         nxt = look(w.t0 + 1);
-        load(kp, row, rk);
-        load(vp, row, rv);
-        bk = ldg1(a.c.ks + max(row, 0), row >= 0);
-        bv = ldg1(a.c.vs + max(row, 0), row >= 0);
-        for (int t = w.t0; t < w.t1 && ok; ++t) {
+        uint32_t byte, byte2;  // the scale byte of the lane's slot: this job's, the next one's
+        load(0, row, byte);
+        shift();
+        load(1, row, byte2);
+        uint32_t word = __ballot_sync(0xffffffffu, row >= 0);
+#pragma unroll 1
+        for (int job = 2 * w.t0; job < 2 * w.t1; ++job) {
+          const int t = job >> 1, v = job & 1;
           const uint32_t s = tc_ % kStages, ph = (tc_ / kStages) & 1;
-          const uint32_t word = __ballot_sync(0xffffffffu, row >= 0);
-          row = pool_row(a, w.h, nxt);
-          nxt = look(t + 2);
-          ok = warp_wait(KE(s), ph ^ 1);
+          ok = warp_wait(v ? VE(s) : KE(s), ph ^ 1);
           if (!ok) break;
-          if (lane == 0) smask[(tc_ & 7) * 4 + pw] = word;
-          store(rk, bk, base + S::oK + s * S::kTileBytes, kTTile);
-          arrive(KF(s));
-          load(kp, row, rk);
-          bk = ldg1(a.c.ks + max(row, 0), row >= 0);
-          if (t == w.t0) {
+          if (!v) {
+            if (lane == 0) smask[(tc_ & 7) * 4 + pw] = word;
+            row = pool_row(a, w.h, nxt);
+            nxt = look(t + 2);
+            word = __ballot_sync(0xffffffffu, row >= 0);
+          }
+          store(byte, base + (v ? S::oV : S::oK) + s * S::kTileBytes,
+                v ? x.seen_min - t * kTTile : kTTile);
+          arrive(v ? VF(s) : KF(s));
+          shift();
+          byte = byte2;
+          load(v, row, byte2);
+          if (job == 2 * w.t0) {
             ok = warp_wait(QE, (units & 1) ^ 1);
             if (!ok) break;
             load_q(x);
             copy_wait<0>();
             arrive(QF);
           }
-          ok = warp_wait(VE(s), ph ^ 1);
-          if (!ok) break;
-          store(rv, bv, base + S::oV + s * S::kTileBytes, x.seen_min - t * kTTile);
-          arrive(VF(s));
-          load(vp, row, rv);
-          bv = ldg1(a.c.vs + max(row, 0), row >= 0);
-          ++tc_;
+          tc_ += v;
         }
       }
       if (!ok) break;
@@ -630,23 +659,30 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
         if (!live) break;
         if (warp_rows) {
           tc_fence_after();
-          uint32_t sr[64];
           const int tok0 = (w.t0 + j) * kTTile, lim = seen - tok0;
           const volatile uint32_t* mw = smask + ((tiles + j) & 7) * 4;
-          const bool masked = tok0 + kTTile > x.seen_min || (mw[0] & mw[1] & mw[2] & mw[3]) != ~0u;
-          auto load_half = [&](int half) {
-            tmem_ld64(tS + 64u * half, sr);
-            if (masked) {
-              const uint32_t wa = mw[2 * half], wb = mw[2 * half + 1];
+          if (tok0 + kTTile > x.seen_min || (mw[0] & mw[1] & mw[2] & mw[3]) != ~0u) {
+            // hidden slots: -inf over their logits
+#pragma unroll 1
+            for (int k = 0; k < 8; ++k) {
+              uint32_t o[16];
+              tmem_ld16(tS + 16u * k, o);
+              const uint32_t word = mw[k >> 1] >> (16 * (k & 1));
 #pragma unroll
-              for (int k = 0; k < 64; ++k)
-                if (64 * half + k >= lim || !(((k < 32 ? wa : wb) >> (k & 31)) & 1)) sr[k] = 0xFF800000u;
+              for (int y = 0; y < 16; ++y)
+                if (16 * k + y >= lim || !((word >> y) & 1)) o[y] = 0xFF800000u;
+              tmem_st16(tS + 16u * k, o);
             }
-          };
+            tmem_st_wait();
+          }
+          // Rolled loops over the halves of the row: straight-line code for all
+          // of it (with the producers' beside it) ran out of the instruction
+          // caches, which cost more than the second TMEM read of S.
           float ya = -CUDART_INF_F, yb = -CUDART_INF_F;
-#pragma unroll
+#pragma unroll 1
           for (int half = 0; half < 2; ++half) {
-            load_half(half);
+            uint32_t sr[64];
+            tmem_ld64(tS + 64u * half, sr);
 #pragma unroll
             for (int k = 0; k < 64; k += 4) {
               ya = fmax3(ya, f32(sr[k]), f32(sr[k + 1]));
@@ -680,9 +716,10 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
           const float mu = m == -CUDART_INF_F ? 0.f : m;
           const uint64_t nmu2 = pk2(-mu, -mu);
           uint64_t l2 = pk2(l, 0.f);
-#pragma unroll
-          for (int half = 1; half >= 0; --half) {  // the upper half is in registers
-            if (half == 0) load_half(0);
+#pragma unroll 1
+          for (int half = 1; half >= 0; --half) {
+            uint32_t sr[64];
+            tmem_ld64(tS + 64u * half, sr);
             uint32_t pw[32];
 #pragma unroll
             for (int k = 0; k < 32; ++k) {
