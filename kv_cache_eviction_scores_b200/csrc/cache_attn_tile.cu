@@ -45,16 +45,19 @@ constexpr int kTMmaWarp = 12;
 constexpr uint64_t kTWaitNs = 2000000000ull;
 constexpr uint32_t kTColO = 256;
 
-template <int D, bool kAlt>
+template <typename TP, int D, bool kAlt>
 struct TileShared {
-  static constexpr int kStages = kAlt ? 3 : 2;
+  static constexpr bool kScaled = sizeof(TP) == 1;
+  static constexpr int kStages = kAlt && !kScaled ? 3 : 2;
+  static constexpr int kRing = !kScaled ? 0 : kAlt ? 4 : 2;  // e4m3 K or V tiles on their way
   static constexpr int kQTiles = kAlt ? 1 : 2;
   static constexpr int kBox = 128 * 128;                   // 128 rows x 64 bf16, 128-byte swizzle
   static constexpr int kTileBytes = D / 64 * kBox;
   static constexpr int kBars = 2 + 4 * kStages + 10;
   static constexpr int oK = kQTiles * kTileBytes;
   static constexpr int oV = oK + kStages * kTileBytes;
-  static constexpr int oBars = oV + kStages * kTileBytes;
+  static constexpr int oRaw = oV + kStages * kTileBytes;
+  static constexpr int oBars = oRaw + kRing * 128 * D;
   static constexpr int oMask = oBars + (kBars + 1) / 2 * 16;  // uint32 [8][4]
   static constexpr int oOdd = oMask + 128;                    // int [2]
   static constexpr int oMisc = oOdd + 16;                     // TMEM base, abort flag
@@ -120,18 +123,8 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
 #undef DKV_O8
 #undef DKV_O32
 }
-// 16 bytes, or zeros when !on; volatile, so that it is issued here and not
-// where the value is used.
-__device__ __forceinline__ uint4 ldg16(const void* p, bool on) {
-  uint4 v;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
-      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
-      "@p ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
-      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
-      : "l"(p), "r"((int)on));
-  return v;
-}
+// One byte, or 0 when !on; volatile, so that it is requested here and not where
+// it is used.
 __device__ __forceinline__ uint32_t ldg1(const uint8_t* p, bool on) {
   uint32_t v;
   asm volatile(
@@ -243,7 +236,7 @@ __device__ __forceinline__ void add_non_finite(const AttnDev& a, int b, int h, i
 
 template <typename TP, int D, bool kAlt>
 __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
-  using S = TileShared<D, kAlt>;
+  using S = TileShared<TP, D, kAlt>;
   constexpr int kStages = S::kStages, kRows = kAlt ? 128 : 256;
   constexpr bool kScaled = sizeof(TP) == 1;
   constexpr int kPieces = D / 8;  // of a staged row
@@ -518,16 +511,21 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
         constexpr int kIn = D / 16, kPer = 32 / kIn, kPass = 32 / kPer;
         const int c = lane % kIn;
         // Jobs: K and V of a tile in turn, by the same code (one copy of it: see
-        // the softmax's loops); the next job's bytes are in flight.
-        uint4 now[kPass], nxt_[kPass];
-        auto load = [&](int v, int row, uint32_t& byte) {
-          const uint8_t* pool = v ? vp : kp;
-#pragma unroll
-          for (int i = 0; i < kPass; ++i) {
-            const int at = __shfl_sync(0xffffffffu, row, i * kPer + lane / kIn);
-            nxt_[i] = ldg16(pool + (size_t)max(at, 0) * D + c * 16, at >= 0);
+        // the softmax's loops).  A ring holds the next kRing jobs' bytes as the
+        // asynchronous copies land; a lane widens what it has copied.
+        constexpr int kRing = S::kRing, kAhead = kRing / 2;  // jobs, tiles
+        const uint32_t ring = base + S::oRaw + pw * (32 * D) + lane * 16;
+        auto issue = [&](int job, int row) {
+          if (job < 2 * w.t1) {
+            const uint8_t* pool = (job & 1 ? vp : kp) + c * 16;
+            const uint32_t dst = ring + (uint32_t)(job % kRing) * (128 * D);
+#pragma unroll 4
+            for (int i = 0; i < kPass; ++i) {
+              const int at = __shfl_sync(0xffffffffu, row, i * kPer + lane / kIn);
+              copy16(dst + i * 512, pool + (size_t)max(at, 0) * D, at >= 0);
+            }
           }
-          byte = ldg1((v ? a.c.vs : a.c.ks) + max(row, 0), row >= 0);
+          copy_commit();
         };
         // widened into a stage
         auto put = [&](const uint32_t (&y)[8], int i, uint32_t dst) {
@@ -548,12 +546,12 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
             y[2 * k + 1] = widen2<0xB3A2>(in[k], f2);
           }
         };
-        auto store = [&](uint32_t byte, uint32_t dst, int part) {
+        auto store = [&](uint32_t src, uint32_t byte, uint32_t dst, int part) {
           const uint32_t own = widen_factors(byte);
-#pragma unroll
+#pragma unroll 4
           for (int i = 0; i < kPass; ++i) {
             uint32_t y[8];
-            widen(now[i], __shfl_sync(0xffffffffu, own, i * kPer + lane / kIn), y);
+            widen(lds16(src + i * 512), __shfl_sync(0xffffffffu, own, i * kPer + lane / kIn), y);
             put(y, i, dst);
           }
           if (part >= kTTile && __all_sync(0xffffffffu, own >> 16 == 0x3F80u)) return;
@@ -580,35 +578,42 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
           }
           if (any) odd();
         };
-        auto shift = [&]() {
+        uint32_t words[kAhead + 1], bk, bv, nk = 0, nv = 0;  // the lane's scale bytes, the next tile's
+        int row = 0;
 #pragma unroll
-          for (int i = 0; i < kPass; ++i) now[i] = nxt_[i];
-        };
-        int row = pool_row(a, w.h, nxt);
-        nxt = look(w.t0 + 1);
-        uint32_t byte, byte2;  // the scale byte of the lane's slot: this job's, the next one's
-        load(0, row, byte);
-        shift();
-        load(1, row, byte2);
-        uint32_t word = __ballot_sync(0xffffffffu, row >= 0);
+        for (int i = 0; i < kAhead; ++i) {
+          row = pool_row(a, w.h, nxt);
+          nxt = look(w.t0 + i + 1);
+          words[i] = __ballot_sync(0xffffffffu, row >= 0);
+          issue(2 * (w.t0 + i), row);
+          issue(2 * (w.t0 + i) + 1, row);
+          if (i == 0) {
+            bk = ldg1(a.c.ks + max(row, 0), row >= 0);
+            bv = ldg1(a.c.vs + max(row, 0), row >= 0);
+          }
+        }
 #pragma unroll 1
         for (int job = 2 * w.t0; job < 2 * w.t1; ++job) {
           const int t = job >> 1, v = job & 1;
           const uint32_t s = tc_ % kStages, ph = (tc_ / kStages) & 1;
+          if (!v) {
+            int r1 = row;  // row of the lane's slot in tile t + 1
+            row = pool_row(a, w.h, nxt);  // and in tile t + kAhead
+            nxt = look(t + kAhead + 1);
+            words[kAhead] = __ballot_sync(0xffffffffu, row >= 0);
+            if (kAhead == 1) r1 = row;
+            nk = ldg1(a.c.ks + max(r1, 0), r1 >= 0);
+            nv = ldg1(a.c.vs + max(r1, 0), r1 >= 0);
+          }
           ok = warp_wait(v ? VE(s) : KE(s), ph ^ 1);
           if (!ok) break;
-          if (!v) {
-            if (lane == 0) smask[(tc_ & 7) * 4 + pw] = word;
-            row = pool_row(a, w.h, nxt);
-            nxt = look(t + 2);
-            word = __ballot_sync(0xffffffffu, row >= 0);
-          }
-          store(byte, base + (v ? S::oV : S::oK) + s * S::kTileBytes,
+          if (!v && lane == 0) smask[(tc_ & 7) * 4 + pw] = words[0];
+          copy_wait<kRing - 1>();
+          store(ring + (uint32_t)(job % kRing) * (128 * D), v ? bv : bk,
+                base + (v ? S::oV : S::oK) + s * S::kTileBytes,
                 v ? x.seen_min - t * kTTile : kTTile);
           arrive(v ? VF(s) : KF(s));
-          shift();
-          byte = byte2;
-          load(v, row, byte2);
+          issue(job + kRing, row);
           if (job == 2 * w.t0) {
             ok = warp_wait(QE, (units & 1) ^ 1);
             if (!ok) break;
@@ -616,7 +621,13 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
             copy_wait<0>();
             arrive(QF);
           }
-          tc_ += v;
+          if (v) {
+            ++tc_;
+            bk = nk;
+            bv = nv;
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) words[i] = words[i + 1];
+          }
         }
       }
       if (!ok) break;
@@ -855,7 +866,7 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
 template <typename TP, int D, bool kAlt>
 cudaError_t launch_tile(const AttnDev& a, cudaStream_t st) {
   const auto kern = k_attn_tile<TP, D, kAlt>;
-  constexpr int smem = TileShared<D, kAlt>::kBytes;
+  constexpr int smem = TileShared<TP, D, kAlt>::kBytes;
   static_assert(smem <= 232448, "shared memory of a CTA");
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
