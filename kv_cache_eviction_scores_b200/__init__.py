@@ -37,9 +37,10 @@ e4m3 with a power-of-two scale per row)::
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import os
+import struct
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -472,45 +473,74 @@ def evict(q, k, v, window: int, pool_kernel: int, keep_counts: Sequence[int],
 # ---- paged cache -----------------------------------------------------------------
 
 
-def _cache(k_pages, v_pages, page_table, k_scale, v_scale) -> Cache:
+# The library's structs as bytes: a decoding step makes two of these calls per
+# layer, and packing takes a fraction of the time of filling a ctypes.Structure
+# (whose layouts these are).
+_CACHE_BYTES = struct.Struct("8i5Q").pack
+_ROWS_BYTES = struct.Struct("2Q6q4i3Q").pack
+_ATTN_BYTES = struct.Struct("3Q6q4ifi2Q").pack
+
+
+@functools.lru_cache(maxsize=None)
+def _packed_calls():
+    """The cache entry points with their structs as bytes: (write, read, attention,
+    attention's workspace)."""
+    L, b, vp, sz = lib(), ctypes.c_char_p, ctypes.c_void_p, ctypes.c_size_t
+    out = []
+    for name, args, res in (("dropkv_cache_write", [b, b, vp, vp], ctypes.c_int32),
+                            ("dropkv_cache_read", [b, b, vp, vp], ctypes.c_int32),
+                            ("dropkv_cache_attention", [b, b, vp, sz, vp, vp], ctypes.c_int32),
+                            ("dropkv_cache_attention_workspace_bytes", [b, b], sz)):
+        fn = L[name]  # an object of its own: the prototypes above stay
+        fn.argtypes, fn.restype = args, res
+        out.append(fn)
+    return tuple(out)
+
+
+def _cache(k_pages, v_pages, page_table, k_scale, v_scale) -> bytes:
     """Checks the pages' tensors and describes them to the library."""
-    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise TypeError(f"{name} must be a CUDA tensor (there is no CPU path)")
-        if t.dim() != 4 or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous [n_pages, Hkv, page_size, d] tensor")
-        if t.dtype not in _PAGE_DTYPES:
-            raise TypeError("pages must be bfloat16, float32 or float8_e4m3fn")
-    if k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype:
+    if not (isinstance(k_pages, torch.Tensor) and isinstance(v_pages, torch.Tensor)
+            and k_pages.is_cuda and v_pages.is_cuda):
+        raise TypeError("k_pages and v_pages must be CUDA tensors (there is no CPU path)")
+    shape = k_pages.shape
+    if len(shape) != 4 or not k_pages.is_contiguous() or not v_pages.is_contiguous():
+        raise ValueError("pages must be contiguous [n_pages, Hkv, page_size, d] tensors")
+    dt = _PAGE_DTYPES.get(k_pages.dtype)
+    if dt is None or v_pages.dtype not in _PAGE_DTYPES:
+        raise TypeError("pages must be bfloat16, float32 or float8_e4m3fn")
+    if v_pages.shape != shape or v_pages.dtype != k_pages.dtype:
         raise ValueError("k_pages and v_pages must have the same shape and dtype")
-    n_pages, Hkv, page_size, d = k_pages.shape
-    dt = _PAGE_DTYPES[k_pages.dtype]
-    _int32_on(page_table, "page_table", k_pages.device)
-    if page_table.dim() != 2:
+    dev = k_pages.device
+    if v_pages.device != dev:
+        raise ValueError("k_pages and v_pages must be on one device")
+    n_pages, Hkv, page_size, d = shape
+    table = _int32_on(page_table, "page_table", dev)
+    if table is None or page_table.dim() != 2:
         raise ValueError("page_table must be [B, max_pages]")
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        if (t is not None) != (dt == E4M3):
-            raise ValueError("e4m3 pages come with k_scale and v_scale, other pages without")
-        if t is None:
-            continue
-        if t.dtype != torch.uint8 or t.device != k_pages.device or not t.is_contiguous():
-            raise TypeError(f"{name} must be a contiguous uint8 tensor on the pages' device")
-        if t.shape != k_pages.shape[:3]:
-            raise ValueError(f"{name} must be [n_pages, Hkv, page_size]")
-    return Cache(page_table.shape[0], Hkv, d, n_pages, page_size, page_table.shape[1], dt, 0,
-                 k_pages.data_ptr(), v_pages.data_ptr(),
-                 None if k_scale is None else k_scale.data_ptr(),
-                 None if v_scale is None else v_scale.data_ptr(), page_table.data_ptr())
+    ks = vs = 0
+    if dt == E4M3 or k_scale is not None or v_scale is not None:
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if (t is not None) != (dt == E4M3):
+                raise ValueError("e4m3 pages come with k_scale and v_scale, other pages without")
+            if t.dtype != torch.uint8 or t.device != dev or not t.is_contiguous():
+                raise TypeError(f"{name} must be a contiguous uint8 tensor on the pages' device")
+            if t.shape != shape[:3]:
+                raise ValueError(f"{name} must be [n_pages, Hkv, page_size]")
+        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
+    B, max_pages = page_table.shape
+    return _CACHE_BYTES(B, Hkv, d, n_pages, page_size, max_pages, dt, 0, k_pages.data_ptr(),
+                        v_pages.data_ptr(), ks, vs, table)
 
 
 def _int32_on(t, name, device, shape=None):
+    """The address of an int32 tensor on the pages' device; None for None."""
     if t is None:
         return None
     if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != device:
         raise TypeError(f"{name} must be an int32 tensor on the pages' device")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have the shape {list(shape)}")
     return t.data_ptr()
 
@@ -521,16 +551,18 @@ def _dense(t, name, device, shape):
         raise TypeError(f"{name} must be a CUDA tensor on the pages' device")
     if t.dtype not in _DENSE_DTYPES:
         raise TypeError(f"{name} must be bfloat16 or float32")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have the shape {list(shape)}")
     st = t.stride()
     if st[3] != 1 and shape[3] != 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
-    return (ctypes.c_int64 * 3)(*st[:3])
+    return st[:3]
 
 
 def _written(t, name):
     """A tensor that a call writes: no element may stand for two indices."""
+    if t.is_contiguous():
+        return
     reach = 1
     for size, stride in sorted(((n, s) for n, s in zip(t.shape, t.stride()) if n > 1),
                                key=lambda x: x[1]):
@@ -539,43 +571,49 @@ def _written(t, name):
         reach = stride * size
 
 
-@contextlib.contextmanager
-def _reported(device, status, sync, what):
-    """The device of a call and its status word; after it, with ``sync``, the
-    wait and the check."""
-    if status is not None and (not status.is_cuda or status.dtype != torch.int32):
-        raise TypeError("status must be a CUDA int32 tensor")
-    if sync and status is None:
+def _launch(fn, what, args, device, status, sync):
+    """Calls fn(*args, status word, stream) on the pages' device; with ``sync``,
+    waits and checks the status."""
+    if status is not None:
+        if status.dtype != torch.int32 or status.device != device or status.numel() < 1:
+            raise TypeError("status must be a CUDA int32 tensor on the pages' device")
+    elif sync:
         status = torch.empty(1, dtype=torch.int32, device=device)
+    word = None if status is None else status.data_ptr()
     if device.index == torch.cuda.current_device():
-        yield status
+        code = fn(*args, word, torch.cuda.current_stream(device).cuda_stream)
     else:
         with torch.cuda.device(device):
-            yield status
+            code = fn(*args, word, torch.cuda.current_stream(device).cuda_stream)
+    if code != OK:
+        _check(code, what)
     if sync:
         torch.cuda.current_stream(device).synchronize()
-        _check(int(status[0].item()), what)
+        _check(int(status.view(-1)[0].item()), what)
 
 
-def _move(fn, what, dense, pages, shape, rows, start, counts, status, sync):
-    k, v, (k_pages, v_pages, page_table, k_scale, v_scale) = *dense, pages
-    c = _cache(k_pages, v_pages, page_table, k_scale, v_scale)
+def _move(fn, what, dense, pages, n, rows, start, counts, status, sync):
+    k, v = dense
+    c = _cache(*pages)
+    k_pages, _, page_table, _, _ = pages
     dev = k_pages.device
-    n = shape[2]
-    m = n if rows is None else rows.shape[-1]
-    ks, vs = _dense(k, "k", dev, shape), _dense(v, "v", dev, shape)
+    B, shape = page_table.shape[0], k_pages.shape
+    Hkv = shape[1]
+    dense_shape = (B, Hkv, n, shape[3])
+    ks, vs = _dense(k, "k", dev, dense_shape), _dense(v, "v", dev, dense_shape)
     if k.dtype != v.dtype:
         raise TypeError("k and v must share one dtype")
-    r = CacheRows(k.data_ptr(), v.data_ptr(), ks, vs, _DENSE_DTYPES[k.dtype], n, m, 0,
-                  _int32_on(rows, "rows", dev, (c.B, c.Hkv, m)),
-                  _int32_on(start, "start", dev, (c.B,)),
-                  _int32_on(counts, "counts", dev, (c.B,)))
+    m = n if rows is None else rows.shape[-1]
+    r = (None if rows is None else _int32_on(rows, "rows", dev, (B, Hkv, m)),
+         None if start is None else _int32_on(start, "start", dev, (B,)),
+         None if counts is None else _int32_on(counts, "counts", dev, (B,)))
     if m == 0 or n == 0:  # nothing to move
         if status is not None:
             status.zero_()
         return
-    with _reported(dev, status, sync, what) as word:
-        _check(fn(ctypes.byref(c), ctypes.byref(r), _ptr(word), _stream(dev)), what)
+    r = _ROWS_BYTES(k.data_ptr(), v.data_ptr(), *ks, *vs, _DENSE_DTYPES[k.dtype], n, m, 0,
+                    r[0] or 0, r[1] or 0, r[2] or 0)
+    _launch(fn, what, (c, r), dev, status, sync)
 
 
 def dropkv_cache_write(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor,
@@ -600,9 +638,8 @@ def dropkv_cache_write(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor,
     device-side status lands there (ERR_ARG: some page, slot, row or count was
     out of range; what it named was left out); ``sync=True`` waits and raises.
     """
-    B, Hkv, n, d = page_table.shape[0], k_pages.shape[1], k.shape[2], k_pages.shape[3]
-    _move(lib().dropkv_cache_write, "dropkv_cache_write", (k, v),
-          (k_pages, v_pages, page_table, k_scale, v_scale), (B, Hkv, n, d), rows, start, counts,
+    _move(_packed_calls()[0], "dropkv_cache_write", (k, v),
+          (k_pages, v_pages, page_table, k_scale, v_scale), k.shape[2], rows, start, counts,
           status, sync)
 
 
@@ -622,21 +659,19 @@ def dropkv_cache_read(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: 
     bf16 or fp32 (default: the pages' own, bf16 for e4m3 pages).  The other
     arguments are dropkv_cache_write's.
     """
-    B, Hkv, d = page_table.shape[0], k_pages.shape[1], k_pages.shape[3]
     if rows is not None and rows.shape[-1] != n:
         raise ValueError("rows must list n slots per (sequence, head)")
     if out is None:
         dtype = dtype or (k_pages.dtype if k_pages.dtype in _DENSE_DTYPES else torch.bfloat16)
-        out = tuple(torch.zeros(B, Hkv, n, d, dtype=dtype, device=k_pages.device)
-                    for _ in range(2))
+        shape = (page_table.shape[0], k_pages.shape[1], n, k_pages.shape[3])
+        out = tuple(torch.zeros(shape, dtype=dtype, device=k_pages.device) for _ in range(2))
     else:
         for name, t in zip(("k", "v"), out):
             _written(t, f"out {name}")
             if dtype is not None and t.dtype != dtype:
                 raise TypeError("out and dtype disagree")
-    _move(lib().dropkv_cache_read, "dropkv_cache_read", out,
-          (k_pages, v_pages, page_table, k_scale, v_scale), (B, Hkv, n, d), rows, start, counts,
-          status, sync)
+    _move(_packed_calls()[1], "dropkv_cache_read", out,
+          (k_pages, v_pages, page_table, k_scale, v_scale), n, rows, start, counts, status, sync)
     return out
 
 
@@ -677,20 +712,22 @@ def dropkv_cache_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torc
     dev = k_pages.device
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise ValueError("q must be [B, Hq, T, d]")
-    B, Hq, T, d = q.shape
-    if (B, d) != (c.B, c.d) or Hq % c.Hkv:
+    shape = q.shape
+    B, Hq, T, d = shape
+    _, Hkv, _, page_d = k_pages.shape
+    if B != page_table.shape[0] or d != page_d or Hq % Hkv:
         raise ValueError("q must be [B, Hq, T, d] with the pages' B and d and Hq a multiple of Hkv")
-    qs = _dense(q, "q", dev, q.shape)
+    qs = _dense(q, "q", dev, shape)
     if out is None:
-        out = torch.zeros(q.shape, dtype=q.dtype, device=dev) if q_lengths is not None else \
-            torch.empty(q.shape, dtype=q.dtype, device=dev)
-    os_ = _dense(out, "out", dev, q.shape)
+        out = torch.zeros(shape, dtype=q.dtype, device=dev) if q_lengths is not None else \
+            torch.empty(shape, dtype=q.dtype, device=dev)
+    os_ = _dense(out, "out", dev, shape)
     _written(out, "out")
     if out.dtype != q.dtype:
         raise TypeError("out must have q's dtype")
     if lse is not None:
         if lse.dtype != torch.float32 or lse.device != dev or not lse.is_contiguous() \
-                or tuple(lse.shape) != (B, Hq, T):
+                or lse.shape != (B, Hq, T):
             raise ValueError("lse must be a contiguous fp32 [B, Hq, T] tensor on the pages' device")
         return_lse = True
     elif return_lse:
@@ -699,23 +736,23 @@ def dropkv_cache_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torc
         raise ValueError("scale must be positive and finite")
     if lengths is None:
         raise ValueError("lengths are needed")
-    a = CacheAttn(q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(), qs, os_,
-                  _DENSE_DTYPES[q.dtype], Hq, T, 1 if causal else 0, scale or 0.0, _PATHS[path],
-                  _int32_on(lengths, "lengths", dev, (B,)),
-                  _int32_on(q_lengths, "q_lengths", dev, (B,)))
+    a = _ATTN_BYTES(q.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(), *qs, *os_,
+                    _DENSE_DTYPES[q.dtype], Hq, T, 1 if causal else 0, scale or 0.0, _PATHS[path],
+                    _int32_on(lengths, "lengths", dev, (B,)),
+                    0 if q_lengths is None else _int32_on(q_lengths, "q_lengths", dev, (B,)))
     if T == 0:  # no rows
         if status is not None:
             status.zero_()
         return (out, lse) if return_lse else out
-    need = cache_attention_workspace_bytes(c, a)
+    _, _, attend, workspace_bytes = _packed_calls()
+    need = workspace_bytes(c, a)
     if need == 0:
         raise DropKVError(ERR_ARG, "dropkv_cache_attention_workspace_bytes")
     if workspace is None or workspace.numel() * workspace.element_size() < need:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    with _reported(dev, status, sync, "dropkv_cache_attention") as word:
-        _check(lib().dropkv_cache_attention(ctypes.byref(c), ctypes.byref(a), _ptr(workspace),
-                                            workspace.numel() * workspace.element_size(),
-                                            _ptr(word), _stream(dev)), "dropkv_cache_attention")
+    _launch(attend, "dropkv_cache_attention",
+            (c, a, workspace.data_ptr(), workspace.numel() * workspace.element_size()), dev, status,
+            sync)
     return (out, lse) if return_lse else out
 
 

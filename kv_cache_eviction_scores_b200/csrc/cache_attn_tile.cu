@@ -28,7 +28,7 @@
 // 0 * NaN must not reach the other rows: the producers stage such values as 0
 // and raise the unit's flag, and the rows that do see them add them at the end.
 //
-// Every wait on an mbarrier is bounded (2 s of %globaltimer); on expiry the
+// Every wait on an mbarrier is bounded (some two seconds); on expiry the
 // kernel records DROPKV_ERR_TIMEOUT, every role leaves, and TMEM is freed.
 #include "cache_attn.cuh"
 #include "tc_ptx.cuh"
@@ -39,11 +39,12 @@ namespace {
 
 using namespace tc;
 
-constexpr int kTThreads = 416, kTTile = 128, kTCtas = 148;
+constexpr int kTThreads = 448, kTTile = 128, kTCtas = 148;
 constexpr int kTProd = 4;                    // producer warps 8..11
-constexpr int kTMmaWarp = 12;
-constexpr uint64_t kTWaitNs = 2000000000ull;
+constexpr int kTMmaWarp = 12;                // 12 and 13: one per query tile (kAlt: per warpgroup)
+constexpr long long kTWaitClocks = 4000000000ll;  // of a wait: two seconds at least
 constexpr uint32_t kTColO = 256;
+
 
 template <typename TP, int D, bool kAlt>
 struct TileShared {
@@ -53,14 +54,14 @@ struct TileShared {
   static constexpr int kQTiles = kAlt ? 1 : 2;
   static constexpr int kBox = 128 * 128;                   // 128 rows x 64 bf16, 128-byte swizzle
   static constexpr int kTileBytes = D / 64 * kBox;
-  static constexpr int kBars = 2 + 4 * kStages + 10;
+  static constexpr int kBars = 2 + 4 * kStages + 11;
   static constexpr int oK = kQTiles * kTileBytes;
   static constexpr int oV = oK + kStages * kTileBytes;
   static constexpr int oRaw = oV + kStages * kTileBytes;
   static constexpr int oBars = oRaw + kRing * 128 * D;
   static constexpr int oMask = oBars + (kBars + 1) / 2 * 16;  // uint32 [8][4]
   static constexpr int oOdd = oMask + 128;                    // int [2]
-  static constexpr int oMisc = oOdd + 16;                     // TMEM base, abort flag
+  static constexpr int oMisc = oOdd + 16;                     // TMEM base
   static constexpr int oXml = oMisc + 16;                     // float2 [2][128], kAlt
   static constexpr int oPlan = oXml + (kAlt ? 2 * 128 * 8 : 0);
   static constexpr int kBytes = oPlan + (int)sizeof(AttnPlanShared);
@@ -69,13 +70,22 @@ struct TileShared {
 __device__ __forceinline__ float f32(uint32_t u) { return __uint_as_float(u); }
 __device__ __forceinline__ uint32_t u32(float f) { return __float_as_uint(f); }
 
-__device__ __forceinline__ void fail(const AttnDev& a, volatile int* abort_flag) {
-  *abort_flag = 1;
+// A wait has run out: this role leaves, and the waits on it run out in turn.
+__device__ __forceinline__ void fail(const AttnDev& a) {
   if (a.status) atomicMax(a.status, (int)DROPKV_ERR_TIMEOUT);
+}
+// Waits are bounded by the SM's clock: reading %globaltimer takes too long for
+// loops that have to see a barrier at once.
+__device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity))
+    if (clock64() - t0 > kTWaitClocks) return false;
+  return true;
 }
 // The outcome is the same for every lane, so the warp stays converged.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, kTWaitNs));
+  return __all_sync(0xffffffffu, wait_on(bar, parity));
 }
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
@@ -171,6 +181,30 @@ __device__ __forceinline__ uint32_t widen2(uint32_t x, uint32_t f) {
   return mul_bf16x2((z << 4) & 0x87F087F0u, f);
 }
 
+// 2^x of two values without the special-function unit: n = x rounded to an
+// integer by the addition of 1.5 2^23, 2^(x - n) on [-1/2, 1/2] by a polynomial of
+// degree 4 fitted for the least relative error (2.9e-6) under p(0) = 1, and n
+// added to the exponent.  x is clamped at -127, which gives exactly 0 there.
+__device__ __forceinline__ void ex2_poly2(float& x0, float& x1) {
+  const uint64_t x = pk2(fmaxf(x0, -127.f), fmaxf(x1, -127.f));
+  const uint64_t t = fadd2(x, pk2(12582912.f, 12582912.f));
+  const uint64_t f = ffma2(fadd2(t, pk2(-12582912.f, -12582912.f)), pk2(-1.f, -1.f), x);
+  uint64_t p = ffma2(pk2(0.009582852f, 0.009582852f), f, pk2(0.055906426f, 0.055906426f));
+  p = ffma2(p, f, pk2(0.24024099f, 0.24024099f));
+  p = ffma2(p, f, pk2(0.6931242f, 0.6931242f));
+  p = ffma2(p, f, pk2(1.f, 1.f));
+  float t0, t1, p0, p1;
+  upk2(t, t0, t1);
+  upk2(p, p0, p1);
+  x0 = f32(u32(p0) + (u32(t0) << 23));
+  x1 = f32(u32(p1) + (u32(t1) << 23));
+}
+__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {  // NaN if one of them is
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // The rows of one unit as a role sees them.
 struct Unit {
   int b, rt, rows, seen_all, seen_min, L, n;
@@ -240,6 +274,12 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
   constexpr int kStages = S::kStages, kRows = kAlt ? 128 : 256;
   constexpr bool kScaled = sizeof(TP) == 1;
   constexpr int kPieces = D / 8;  // of a staged row
+  // Of 8 exponentials, those on the FMA pipe (the special-function unit does 16 a
+  // clock), and the half of P whose end starts the second query tile.  Measured
+  // (512 tokens over 32K bf16 slots; 4 x 2048 over e4m3, whose widening fills the
+  // ALU pipe): 0 to 4 of 8 352, 349, 331, 349, 353 and 821, 792, 806, 826, 847 us;
+  // no delay, upper half, lower half 331, 319, 309 and 791, 764, 808 us.
+  constexpr int kTPoly = kScaled ? 1 : 2, kGoHalf = kScaled ? 1 : 0;
   extern __shared__ __align__(1024) uint8_t sm[];
   pdl_trigger();
   const uint32_t base = smem_u32(sm);
@@ -252,7 +292,6 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
   }
   AttnPlanShared& plan = *reinterpret_cast<AttnPlanShared*>(sm + S::oPlan);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + S::oMisc);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + S::oMisc + 4);
   volatile uint32_t* smask = reinterpret_cast<volatile uint32_t*>(sm + S::oMask);
   volatile int* sodd = reinterpret_cast<volatile int*>(sm + S::oOdd);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -271,14 +310,17 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
   auto PD = [&](int u) { return bar(kB0 + 6 + u); };
   // units of even / odd number finished by the softmax warps
   auto UE = [&](int p) { return bar(kB0 + 8 + p); };
+  // a unit's second query tile begins
+  const uint32_t GO = bar(kB0 + 10);
   if (threadIdx.x == 0) {
+    mbar_init(GO, 1);
     mbar_init(QF, kTProd);
-    mbar_init(QE, 1);
+    mbar_init(QE, 2);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(KF(s), kTProd);
-      mbar_init(KE(s), 1);
+      mbar_init(KE(s), kAlt ? 1 : 2);
       mbar_init(VF(s), kTProd);
-      mbar_init(VE(s), 1);
+      mbar_init(VE(s), kAlt ? 1 : 2);
     }
     for (int u = 0; u < 2; ++u) {
       mbar_init(SF(u), 1);
@@ -288,7 +330,6 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
       mbar_init(UE(u), 8);
       sodd[u] = 0;
     }
-    *abort_flag = 0;
     a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
     fence_mbar_init();
   }
@@ -306,96 +347,92 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
   const uint32_t tbase = *tmem_slot;
 
   if (warp >= kTMmaWarp) {
-    if (warp == kTMmaWarp) {
-      // ---------------- MMA issuer ----------------
-      constexpr uint32_t IDS = idesc_bf16(128, 128, false, false);  // S = Q K^T
-      constexpr uint32_t IDP = idesc_bf16(128, D, false, true);     // O += P V (V MN-major)
-      const SDesc qd = sdesc_split(base, 16, 1024);
-      const SDesc kd = sdesc_split(base + S::oK, 16, 1024);
-      const SDesc vd = sdesc_split(base + S::oV, S::kBox, 1024);
-      uint32_t kc = 0, vc = 0;             // slot tiles whose S / P V are all issued
-      uint32_t ns[2] = {0, 0}, np[2] = {0, 0};  // S and P V issued per warpgroup
-      uint32_t units = 0;
-      bool ok = true;
-      // S = Q_q K^T of the kc-th tile into warpgroup u's columns, once the P V
-      // that reads its last P from there is done
-      auto issue_S = [&](int u, int q, bool last_of_tile, bool last_of_unit) {
-        const uint32_t s = kc % kStages;
-        if (!warp_wait(KF(s), (kc / kStages) & 1)) return false;
-        if (ns[u] >= 1 && !warp_wait(PD(u), (ns[u] - 1) & 1)) return false;
+    // ---------------- MMA issuers ----------------
+    // Warp u: S and P V of query tile u (kAlt: of the slot tiles j = u mod 2), so
+    // that no tile's products wait for the other's softmax.  Measured against one
+    // warp for both, in turn or as they became ready: 331 against 350 and 377 us
+    // for 512 tokens over 32K bf16 slots (an MMA is issued as it executes, 64
+    // clocks, and a barrier seen some 100 clocks late).
+    const int u = warp - kTMmaWarp;
+    constexpr int kStep = kAlt ? 2 : 1;
+    constexpr uint32_t IDS = idesc_bf16(128, 128, false, false);  // S = Q K^T
+    constexpr uint32_t IDP = idesc_bf16(128, D, false, true);     // O += P V (V MN-major)
+    const SDesc qd = sdesc_split(base + (kAlt ? 0 : u * S::kTileBytes), 16, 1024);
+    const SDesc kd = sdesc_split(base + S::oK, 16, 1024);
+    const SDesc vd = sdesc_split(base + S::oV, S::kBox, 1024);
+    const uint32_t dS = tbase + 128u * u, dO = tbase + kTColO + 128u * u;
+    uint32_t tiles = 0, units = 0;  // of the range so far
+    uint32_t n = 0;                 // P V issued by this warp
+    bool ok = true;
+    while (more && ok) {
+      const Unit x = unit_of<kRows>(a, w);
+      const int T = w.t1 - w.t0;
+      // a stage is handed back by both warps; a single query tile's does it twice
+      const bool twice = !kAlt && x.rows <= 128;
+      ok = warp_wait(QF, units & 1);
+      ++units;
+      tc_fence_after();
+      // S of tile j, once the P V that reads the last P from its columns is done
+      auto issue_S = [&](int j) {
+        const uint32_t i = tiles + j, s = i % kStages;
+        if (!warp_wait(KF(s), (i / kStages) & 1)) return false;
+        if (n >= 1 && !warp_wait(PD(u), (n - 1) & 1)) return false;
         tc_fence_after();
         if (lane == 0) {
-          const uint32_t qlo = qd.lo + (uint32_t)q * (S::kTileBytes >> 4);
           const uint32_t klo = kd.lo + s * (S::kTileBytes >> 4);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t at = (uint32_t)((kk >> 2) * (S::kBox >> 4) + (kk & 3) * 2);
-            mma_ss_w(tbase + 128u * u, qlo + at, qd.hi, klo + at, kd.hi, IDS, kk > 0 ? 1u : 0u);
+            mma_ss_w(dS, qd.lo + at, qd.hi, klo + at, kd.hi, IDS, kk > 0 ? 1u : 0u);
           }
           mma_commit(SF(u));
-          if (last_of_tile) mma_commit(KE(s));
-          if (last_of_unit) mma_commit(QE);
+          mma_commit(KE(s));
+          if (twice) mma_commit(KE(s));
+          if (j + kStep >= T) mma_commit(QE);
         }
         __syncwarp();
-        ++ns[u];
-        if (last_of_tile) ++kc;
         return true;
       };
-      // O_u (+)= P_u V of the vc-th tile
-      auto issue_PV = [&](int u, bool first, bool last_of_tile) {
-        const uint32_t s = vc % kStages;
-        if (!warp_wait(VF(s), (vc / kStages) & 1)) return false;
-        const uint32_t vlo = vd.lo + s * (S::kTileBytes >> 4);
-        const uint32_t dO = tbase + kTColO + 128u * u, pS = tbase + 128u * u;
+      const int first = kAlt ? u : 0;
+      if (kAlt ? first < T : 128 * u < x.rows) {
+        // The second query tile begins half a tile late: in step, the two would
+        // take turns to leave the tensor pipe and the special-function unit idle.
+        if (!kAlt && u == 1) ok = ok && warp_wait(GO, (units - 1) & 1);
+        ok = ok && issue_S(first);
+        for (int j = first; j < T && ok; j += kStep) {
+          // O (+)= P V of tile j, as the halves of P come
+          const uint32_t i = tiles + j, s = i % kStages;
+          const uint32_t vlo = vd.lo + s * (S::kTileBytes >> 4);
+          ok = warp_wait(VF(s), (i / kStages) & 1);
 #pragma unroll
-        for (int half = 1; half >= 0; --half) {
-          if (!warp_wait(half ? PA(u) : PB(u), np[u] & 1)) return false;
-          tc_fence_after();
-          if (lane == 0) {
+          for (int half = 1; half >= 0; --half) {
+            ok = ok && warp_wait(half ? PA(u) : PB(u), n & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (lane == 0) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)  // V slices of 16 rows, 2 KB
-              mma_ts_w(dO, pS + 64u * half + 8u * kk, vlo + 128u * (4 * half + kk), vd.hi, IDP,
-                       (!first || half == 0 || kk > 0) ? 1u : 0u);
-          }
-        }
-        if (lane == 0) {
-          mma_commit(PD(u));
-          if (last_of_tile) mma_commit(VE(s));
-        }
-        __syncwarp();
-        ++np[u];
-        if (last_of_tile) ++vc;
-        return true;
-      };
-      while (more && ok) {
-        const Unit x = unit_of<kRows>(a, w);
-        const int T = w.t1 - w.t0;
-        ok = warp_wait(QF, units & 1);
-        ++units;
-        tc_fence_after();
-        if (kAlt) {
-          for (int j = 0; j < 2 && j < T && ok; ++j) ok = issue_S(j, 0, true, j == T - 1);
-          for (int j = 0; j < T && ok; ++j) {
-            ok = issue_PV(j & 1, j < 2, true);
-            if (ok && j + 2 < T) ok = issue_S(j & 1, 0, true, j + 2 == T - 1);
-          }
-        } else {
-          const int nt = x.rows > 128 ? 2 : 1;
-          for (int u = 0; u < nt && ok; ++u) ok = issue_S(u, u, u == nt - 1, T == 1 && u == nt - 1);
-          for (int j = 0; j < T && ok; ++j)
-            for (int u = 0; u < nt && ok; ++u) {
-              ok = issue_PV(u, j == 0, u == nt - 1);
-              if (ok && j + 1 < T)
-                ok = issue_S(u, u, u == nt - 1, j + 1 == T - 1 && u == nt - 1);
+              for (int kk = 0; kk < 4; ++kk)  // V slices of 16 rows, 2 KB
+                mma_ts_w(dO, dS + 64u * half + 8u * kk, vlo + 128u * (4 * half + kk), vd.hi, IDP,
+                         (j != first || half == 0 || kk > 0) ? 1u : 0u);
             }
+          }
+          if (!ok) break;
+          if (lane == 0) {
+            mma_commit(PD(u));
+            mma_commit(VE(s));
+            if (twice) mma_commit(VE(s));
+          }
+          __syncwarp();
+          ++n;
+          if (j + kStep < T) ok = issue_S(j + kStep);
         }
-        if (!ok) {
-          if (lane == 0) fail(a, abort_flag);
-          break;
-        }
-        more = attn_next<kRows, kTTile>(a, w);
+      } else if (lane == 0) {
+        mbar_arrive(QE);  // nothing to read; but no unit passes without this warp
       }
+      tiles += T;
+      more = attn_next<kRows, kTTile>(a, w);
     }
+    if (!ok && lane == 0) fail(a);
   } else if (warp >= 8) {
     // ---------------- producers ----------------
     // Warp pw stages the slots 32 pw .. 32 pw + 31 of every tile, and the
@@ -519,11 +556,13 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
           if (job < 2 * w.t1) {
             const uint8_t* pool = (job & 1 ? vp : kp) + c * 16;
             const uint32_t dst = ring + (uint32_t)(job % kRing) * (128 * D);
-#pragma unroll 4
-            for (int i = 0; i < kPass; ++i) {
-              const int at = __shfl_sync(0xffffffffu, row, i * kPer + lane / kIn);
-              copy16(dst + i * 512, pool + (size_t)max(at, 0) * D, at >= 0);
-            }
+            int at[kPass];
+#pragma unroll
+            for (int i = 0; i < kPass; ++i)
+              at[i] = __shfl_sync(0xffffffffu, row, i * kPer + lane / kIn);
+#pragma unroll
+            for (int i = 0; i < kPass; ++i)
+              copy16(dst + i * 512, pool + (size_t)max(at[i], 0) * D, at[i] >= 0);
           }
           copy_commit();
         };
@@ -548,11 +587,23 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
         };
         auto store = [&](uint32_t src, uint32_t byte, uint32_t dst, int part) {
           const uint32_t own = widen_factors(byte);
-#pragma unroll 4
-          for (int i = 0; i < kPass; ++i) {
-            uint32_t y[8];
-            widen(lds16(src + i * 512), __shfl_sync(0xffffffffu, own, i * kPer + lane / kIn), y);
-            put(y, i, dst);
+          // four passes' loads before their conversions: a warp alone on its
+          // scheduler has nobody else to hide their latency
+#pragma unroll 1
+          for (int i0 = 0; i0 < kPass; i0 += 4) {
+            uint4 in[4];
+            uint32_t f[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              in[i] = lds16(src + (i0 + i) * 512);
+              f[i] = __shfl_sync(0xffffffffu, own, (i0 + i) * kPer + lane / kIn);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t y[8];
+              widen(in[i], f[i], y);
+              put(y, i0 + i, dst);
+            }
           }
           if (part >= kTTile && __all_sync(0xffffffffu, own >> 16 == 0x3F80u)) return;
           // large scales, or partly seen slots (from row `part` of the tile on),
@@ -634,7 +685,7 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
       ++units;
       more = attn_next<kRows, kTTile>(a, w);
     }
-    if (!ok && lane == 0) fail(a, abort_flag);
+    if (!ok && lane == 0) fail(a);
     copy_wait<0>();
   } else {
     // ---------------- softmax ----------------
@@ -651,8 +702,8 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
     uint32_t tiles = 0, units = 0;
     bool live = true;            // no wait has run out
     auto alive = [&](bool got) {
-      if (!got || __any_sync(0xffffffffu, *abort_flag != 0)) {
-        if (!got && lane == 0) fail(a, abort_flag);
+      if (!got) {
+        if (live && lane == 0) fail(a);
         live = false;
       }
     };
@@ -696,11 +747,12 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
             tmem_ld64(tS + 64u * half, sr);
 #pragma unroll
             for (int k = 0; k < 64; k += 4) {
-              ya = fmax3(ya, f32(sr[k]), f32(sr[k + 1]));
-              yb = fmax3(yb, f32(sr[k + 2]), f32(sr[k + 3]));
+              ya = fmax3_nan(ya, f32(sr[k]), f32(sr[k + 1]));
+              yb = fmax3_nan(yb, f32(sr[k + 2]), f32(sr[k + 3]));
             }
           }
-          const float mt = fmaxf(ya, yb) * c;  // c > 0
+          const float mt = fmax3_nan(ya, yb, -CUDART_INF_F) * c;  // c > 0
+          if (!(mt < CUDART_INF_F)) l = CUDART_NAN_F;  // so is the row, whatever becomes of P
           float fac = 1.f;
           if (mt > m + 8.f) {
             fac = m == -CUDART_INF_F ? 0.f : attn_ex2(m - mt);
@@ -736,7 +788,13 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
             for (int k = 0; k < 32; ++k) {
               float d0, d1;
               upk2(ffma2(pk2(f32(sr[2 * k]), f32(sr[2 * k + 1])), c2, nmu2), d0, d1);
-              const float e0 = attn_ex2(d0), e1 = attn_ex2(d1);
+              float e0 = d0, e1 = d1;
+              if (k % 8 < kTPoly) {
+                ex2_poly2(e0, e1);
+              } else {
+                e0 = attn_ex2(d0);
+                e1 = attn_ex2(d1);
+              }
               l2 = fadd2(l2, pk2(e0, e1));
               pw[k] = pack_bf16(e0, e1);
             }
@@ -745,6 +803,7 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(half ? PA(u) : PB(u));
+            if (!kAlt && half == kGoHalf && j == 0 && threadIdx.x == 0) mbar_arrive(GO);
           }
           float la, lb;
           upk2(l2, la, lb);

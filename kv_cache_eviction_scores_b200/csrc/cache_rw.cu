@@ -92,21 +92,31 @@ __device__ __forceinline__ void put_one(__nv_bfloat16* p, float x) { *p = __floa
 __device__ __forceinline__ void put_one(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put_one(E4M3* p, float x) { p->bits = (uint8_t)pack_e4m3(x, 0.f); }
 
-// Eight values of the row that starts at `p`, values past d as 0.
+// A lane's eight values of a row: as they are stored (kVec), or widened one by
+// one; values past d are 0.
 template <bool kVec, typename T>
-__device__ __forceinline__ void load8(const T* p, int lane, int d, float (&x)[8]) {
-  if (kVec) {
-    if (lane * 8 < d) {
-      widen(*reinterpret_cast<const Eight<T>*>(p + lane * 8), x);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = 0.f;
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = lane + 32 * j < d ? one(p + lane + 32 * j) : 0.f;
+struct Piece {};
+template <typename T>
+struct Piece<true, T> {
+  Eight<T> s;
+  __device__ __forceinline__ void load(const T* p, int lane, int d) {
+    s = Eight<T>{};
+    if (lane * 8 < d) s = *reinterpret_cast<const Eight<T>*>(p + lane * 8);
   }
-}
+  __device__ __forceinline__ void get(float (&x)[8]) const { widen(s, x); }
+};
+template <typename T>
+struct Piece<false, T> {
+  float v[8];
+  __device__ __forceinline__ void load(const T* p, int lane, int d) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = lane + 32 * j < d ? one(p + lane + 32 * j) : 0.f;
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = v[j];
+  }
+};
 template <bool kVec, typename T>
 __device__ __forceinline__ void store8(T* p, int lane, int d, const float (&x)[8]) {
   if (kVec) {
@@ -169,6 +179,15 @@ __device__ __forceinline__ Move find(const CacheDev& c, const RowsDev& r, int b,
   return mv;
 }
 
+template <bool kFirst, typename A, typename B>
+struct Pick {
+  using type = A;
+};
+template <typename A, typename B>
+struct Pick<false, A, B> {
+  using type = B;
+};
+
 template <bool kWrite, bool kVec, typename TD, typename TP, int kRowsInFlight>
 __global__ void __launch_bounds__(kThreads) k_cache_rows(const CacheDev c, const RowsDev r) {
   const int bh = blockIdx.x / r.nblk, blk = blockIdx.x - bh * r.nblk;
@@ -194,63 +213,62 @@ __global__ void __launch_bounds__(kThreads) k_cache_rows(const CacheDev c, const
 #pragma unroll
   for (int u = 0; u < kRowsInFlight; ++u)
     mv[u] = find<kWrite>(c, r, b, h, i0 + u * per, cnt, base);
-  float xk[kRowsInFlight][8], xv[kRowsInFlight][8];
-  if (kWrite) {
+  using From = typename Pick<kWrite, TD, TP>::type;
+  Piece<kVec, From> xk[kRowsInFlight], xv[kRowsInFlight];
+  uint32_t bk[kRowsInFlight], bv[kRowsInFlight];
 #pragma unroll
-    for (int u = 0; u < kRowsInFlight; ++u) {
-      const int dd = mv[u].dense < 0 ? 0 : c.d;  // a row of nothing loads nothing
-      const int64_t row = mv[u].dense < 0 ? 0 : mv[u].dense;
-      load8<kVec>(dk + row * r.ks[2], lane, dd, xk[u]);
-      load8<kVec>(dv + row * r.vs[2], lane, dd, xv[u]);
-    }
-#pragma unroll
-    for (int u = 0; u < kRowsInFlight; ++u) {
-      uint32_t bk = 0, bv = 0;
-      if (kScaled) {
-        bk = to_scaled(xk[u], r.lanes);
-        bv = to_scaled(xv[u], r.lanes);
+  for (int u = 0; u < kRowsInFlight; ++u) {
+    const bool on = mv[u].dense >= 0;  // a row of nothing loads nothing
+    const int dd = on ? c.d : 0;
+    if constexpr (kWrite) {
+      const int64_t row = on ? mv[u].dense : 0;
+      xk[u].load(dk + row * r.ks[2], lane, dd);
+      xv[u].load(dv + row * r.vs[2], lane, dd);
+    } else {
+      const int64_t row = on ? mv[u].held : 0;
+      xk[u].load(pk + row * c.d, lane, dd);
+      xv[u].load(pv + row * c.d, lane, dd);
+      if (kScaled && on) {
+        bk[u] = __ldg(c.ks + row);
+        bv[u] = __ldg(c.vs + row);
       }
-      if (mv[u].dense < 0) continue;
-      store8<kVec>(pk + mv[u].held * c.d, lane, c.d, xk[u]);
-      store8<kVec>(pv + mv[u].held * c.d, lane, c.d, xv[u]);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kRowsInFlight; ++u) {
+    float yk[8], yv[8];
+    xk[u].get(yk);
+    xv[u].get(yv);
+    if (kWrite && kScaled) {  // every lane of the warp
+      bk[u] = to_scaled(yk, r.lanes);
+      bv[u] = to_scaled(yv, r.lanes);
+    }
+    if (mv[u].dense < 0) continue;
+    if constexpr (kWrite) {
+      store8<kVec>(pk + mv[u].held * c.d, lane, c.d, yk);
+      store8<kVec>(pv + mv[u].held * c.d, lane, c.d, yv);
       if (kScaled && lane == 0) {
-        c.ks[mv[u].held] = (uint8_t)bk;
-        c.vs[mv[u].held] = (uint8_t)bv;
+        c.ks[mv[u].held] = (uint8_t)bk[u];
+        c.vs[mv[u].held] = (uint8_t)bv[u];
       }
-    }
-  } else {
-    float fk[kRowsInFlight], fv[kRowsInFlight];
-#pragma unroll
-    for (int u = 0; u < kRowsInFlight; ++u) {
-      const int dd = mv[u].dense < 0 ? 0 : c.d;
-      const int64_t row = mv[u].dense < 0 ? 0 : mv[u].held;
-      load8<kVec>(pk + row * c.d, lane, dd, xk[u]);
-      load8<kVec>(pv + row * c.d, lane, dd, xv[u]);
-      fk[u] = fv[u] = 1.f;
-      if (kScaled && dd) {
-        fk[u] = scale_of(__ldg(c.ks + row));
-        fv[u] = scale_of(__ldg(c.vs + row));
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kRowsInFlight; ++u) {
-      if (mv[u].dense < 0) continue;
+    } else {
       if (kScaled) {
+        const float fk = scale_of(bk[u]), fv = scale_of(bv[u]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          xk[u][j] *= fk[u];
-          xv[u][j] *= fv[u];
+          yk[j] *= fk;
+          yv[j] *= fv;
         }
       }
-      store8<kVec>(dk + mv[u].dense * r.ks[2], lane, c.d, xk[u]);
-      store8<kVec>(dv + mv[u].dense * r.vs[2], lane, c.d, xv[u]);
+      store8<kVec>(dk + mv[u].dense * r.ks[2], lane, c.d, yk);
+      store8<kVec>(dv + mv[u].dense * r.vs[2], lane, c.d, yv);
     }
   }
 }
 
 template <bool kWrite, bool kVec, typename TD, typename TP>
 cudaError_t launch_rows(const CacheDev& c, RowsDev r, cudaStream_t st) {
-  constexpr int kFly = kVec ? 2 : 1;
+  constexpr int kFly = kVec ? 4 : 1;
   if (kVec) {
     r.lanes = 1;
     while (r.lanes * 8 < c.d) r.lanes *= 2;
