@@ -219,6 +219,11 @@ def _stream(device) -> ctypes.c_void_p:
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
+# The current stream's handle without a torch.cuda.Stream around it (2 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def make_shape(q: torch.Tensor, k: torch.Tensor, window: int, pool_kernel: int) -> Shape:
     B, Hq, w, d = q.shape
     Bk, Hkv, n_max, dk = k.shape
@@ -502,30 +507,28 @@ def _cache(k_pages, v_pages, page_table, k_scale, v_scale) -> bytes:
     if not (isinstance(k_pages, torch.Tensor) and isinstance(v_pages, torch.Tensor)
             and k_pages.is_cuda and v_pages.is_cuda):
         raise TypeError("k_pages and v_pages must be CUDA tensors (there is no CPU path)")
-    shape = k_pages.shape
-    if len(shape) != 4 or not k_pages.is_contiguous() or not v_pages.is_contiguous():
-        raise ValueError("pages must be contiguous [n_pages, Hkv, page_size, d] tensors")
-    dt = _PAGE_DTYPES.get(k_pages.dtype)
+    shape, dev, dtype = k_pages.shape, k_pages.device, k_pages.dtype
+    dt = _PAGE_DTYPES.get(dtype)
     if dt is None or v_pages.dtype not in _PAGE_DTYPES:
         raise TypeError("pages must be bfloat16, float32 or float8_e4m3fn")
-    if v_pages.shape != shape or v_pages.dtype != k_pages.dtype:
-        raise ValueError("k_pages and v_pages must have the same shape and dtype")
-    dev = k_pages.device
-    if v_pages.device != dev:
-        raise ValueError("k_pages and v_pages must be on one device")
+    if len(shape) != 4 or not k_pages.is_contiguous() or not v_pages.is_contiguous():
+        raise ValueError("pages must be contiguous [n_pages, Hkv, page_size, d] tensors")
+    if v_pages.shape != shape or v_pages.dtype != dtype or v_pages.device != dev:
+        raise ValueError("k_pages and v_pages must agree in shape, dtype and device")
     n_pages, Hkv, page_size, d = shape
     table = _int32_on(page_table, "page_table", dev)
     if table is None or page_table.dim() != 2:
         raise ValueError("page_table must be [B, max_pages]")
     ks = vs = 0
     if dt == E4M3 or k_scale is not None or v_scale is not None:
-        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-            if (t is not None) != (dt == E4M3):
-                raise ValueError("e4m3 pages come with k_scale and v_scale, other pages without")
+        if dt != E4M3 or k_scale is None or v_scale is None:
+            raise ValueError("e4m3 pages come with k_scale and v_scale, other pages without")
+        rows = shape[:3]
+        for t in (k_scale, v_scale):
             if t.dtype != torch.uint8 or t.device != dev or not t.is_contiguous():
-                raise TypeError(f"{name} must be a contiguous uint8 tensor on the pages' device")
-            if t.shape != shape[:3]:
-                raise ValueError(f"{name} must be [n_pages, Hkv, page_size]")
+                raise TypeError("scales must be contiguous uint8 tensors on the pages' device")
+            if t.shape != rows:
+                raise ValueError("scales must be [n_pages, Hkv, page_size]")
         ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
     B, max_pages = page_table.shape
     return _CACHE_BYTES(B, Hkv, d, n_pages, page_size, max_pages, dt, 0, k_pages.data_ptr(),
@@ -581,10 +584,10 @@ def _launch(fn, what, args, device, status, sync):
         status = torch.empty(1, dtype=torch.int32, device=device)
     word = None if status is None else status.data_ptr()
     if device.index == torch.cuda.current_device():
-        code = fn(*args, word, torch.cuda.current_stream(device).cuda_stream)
+        code = fn(*args, word, _raw_stream(device.index))
     else:
         with torch.cuda.device(device):
-            code = fn(*args, word, torch.cuda.current_stream(device).cuda_stream)
+            code = fn(*args, word, _raw_stream(device.index))
     if code != OK:
         _check(code, what)
     if sync:
@@ -748,11 +751,14 @@ def dropkv_cache_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torc
     need = workspace_bytes(c, a)
     if need == 0:
         raise DropKVError(ERR_ARG, "dropkv_cache_attention_workspace_bytes")
-    if workspace is None or workspace.numel() * workspace.element_size() < need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _launch(attend, "dropkv_cache_attention",
-            (c, a, workspace.data_ptr(), workspace.numel() * workspace.element_size()), dev, status,
-            sync)
+    if workspace is not None:
+        if not isinstance(workspace, torch.Tensor) or workspace.device != dev \
+                or not workspace.is_contiguous():
+            raise TypeError("workspace must be a contiguous tensor on the pages' device")
+        size = workspace.numel() * workspace.element_size()
+    if workspace is None or size < need:
+        workspace, size = torch.empty(need, dtype=torch.uint8, device=dev), need
+    _launch(attend, "dropkv_cache_attention", (c, a, workspace.data_ptr(), size), dev, status, sync)
     return (out, lse) if return_lse else out
 
 

@@ -4,6 +4,8 @@
 
 #include <cuda_fp8.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -92,6 +94,40 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+
+// Two e4m3 bytes of x to a bf16 pair, times 2^-120 f: the bytes, sign-extended to
+// 16 bits each, four bits up, less the copies of the sign between sign and
+// exponent; so the seven magnitude bits end at the bottom of bf16's exponent and
+// the top of its mantissa (subnormals land on subnormals).  Two instructions of
+// the ALU pipe and two of the FMA pipe (the shift is a product there).
+constexpr uint32_t kBytes01 = 0x9180u, kBytes23 = 0xB3A2u, kBytes02 = 0xA280u, kBytes13 = 0xB391u;
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <uint32_t kSel>
+__device__ __forceinline__ uint32_t widen_e4m3x2(uint32_t x, uint32_t f) {
+  uint32_t z;
+  asm("prmt.b32 %0, %1, %1, %2;" : "=r"(z) : "r"(x), "n"(kSel));
+  return mul_bf16x2((z << 4) & 0x87F087F0u, f);
+}
+
 CacheDev cache_dev(const dropkv_cache& c);
+
+// Allows `kern` `bytes` of dynamic shared memory, once per device (the bit of a
+// device is set after the call that does it, so calls at once do it twice).
+template <auto kern>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 }  // namespace dropkv

@@ -54,21 +54,24 @@ int path_of(const dropkv_cache& c, const dropkv_cache_attn& t) {
   return t.path == DROPKV_PATH_TENSOR ? -1 : DROPKV_PATH_SIMT;
 }
 
-// The tensor path's kernel by the rows a KV head can have: one block of the
-// row kernel, or query tiles of 128 rows.
-enum class Tensor { kRows, kTile128, kTile256 };
+// The tensor path's kernel by the rows a KV head can have: eight as columns, or
+// 16 as rows, of warp-level products; or query tiles of 128 rows.
+enum class Tensor { kFew, kRows, kTile128, kTile256 };
 Tensor tensor_of(const dropkv_cache& c, const dropkv_cache_attn& t) {
   const int64_t rows = (int64_t)(t.Hq / c.Hkv) * t.T;
-  return rows <= 16 ? Tensor::kRows : rows <= 128 ? Tensor::kTile128 : Tensor::kTile256;
+  return rows <= 8     ? Tensor::kFew
+         : rows <= 16  ? Tensor::kRows
+         : rows <= 128 ? Tensor::kTile128
+                       : Tensor::kTile256;
 }
-AttnGrid grid_of(Tensor k) {
-  return k == Tensor::kRows ? attn_grid_rows() : attn_grid_tile(k == Tensor::kTile128);
+AttnGrid grid_of(Tensor k, int page_dtype) {
+  return k == Tensor::kFew    ? attn_grid_few(page_dtype)
+         : k == Tensor::kRows ? attn_grid_rows()
+                              : attn_grid_tile(k == Tensor::kTile128);
 }
 
-size_t layout(const dropkv_cache& c, const AttnGrid& g, size_t* part) {
-  const size_t desc = align_up((size_t)g.ctas * sizeof(int4), 256);
-  if (part) *part = desc;
-  return desc + (size_t)2 * g.ctas * g.rows * ((c.d + 3) / 4 * 4 + 4) * sizeof(float);
+size_t layout(const dropkv_cache& c, const AttnGrid& g) {
+  return (size_t)2 * g.ctas * g.rows * ((c.d + 3) / 4 * 4 + 4) * sizeof(float);
 }
 
 }  // namespace
@@ -81,9 +84,9 @@ extern "C" size_t dropkv_cache_attention_workspace_bytes(const dropkv_cache* cac
                                                          const dropkv_cache_attn* attn) {
   if (check_attn(cache, attn, false) != DROPKV_OK) return 0;
   // the alignment of q and out is not known here: enough for either path
-  const size_t simt = layout(*cache, attn_grid_simt(), nullptr);
+  const size_t simt = layout(*cache, attn_grid_simt());
   if (attn->path == DROPKV_PATH_SIMT || !tensor_sizes(*cache, *attn)) return simt;
-  const size_t tensor = layout(*cache, grid_of(tensor_of(*cache, *attn)), nullptr);
+  const size_t tensor = layout(*cache, grid_of(tensor_of(*cache, *attn), cache->dtype));
   return std::max(simt, tensor);
 }
 
@@ -116,7 +119,7 @@ extern "C" dropkv_status dropkv_cache_attention(const dropkv_cache* cache,
 
   const bool tensor = path == DROPKV_PATH_TENSOR;
   const Tensor kind = tensor_of(c, t);
-  const AttnGrid g = tensor ? grid_of(kind) : attn_grid_simt();
+  const AttnGrid g = tensor ? grid_of(kind, c.dtype) : attn_grid_simt();
   AttnDev a = {};
   a.c = cache_dev(c);
   a.q = t.q;
@@ -136,19 +139,18 @@ extern "C" dropkv_status dropkv_cache_attention(const dropkv_cache* cache,
   a.c_log2 = (float)(scale * 1.4426950408889634);
   a.lengths = t.lengths;
   a.q_lengths = t.q_lengths;
-  size_t part;
-  layout(c, g, &part);
-  a.desc = reinterpret_cast<int4*>(workspace);
-  a.part = reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) + part);
+  a.part = reinterpret_cast<float*>(workspace);
   a.pstride = (c.d + 3) / 4 * 4 + 4;
   a.status = status_dev;
   cudaError_t e;
   if (!tensor)
     e = launch_attn_simt(a, c.dtype, t.dtype, st);
+  else if (kind == Tensor::kFew)
+    e = launch_attn_few(a, c.dtype, st);
   else if (kind == Tensor::kRows)
     e = launch_attn_rows(a, c.dtype, st);
   else
     e = launch_attn_tile(a, c.dtype, kind == Tensor::kTile128, st);
-  if (e == cudaSuccess) e = launch_attn_merge(a, g.ctas, g.rows, t.dtype, st);
+  if (e == cudaSuccess) e = launch_attn_merge(a, g, t.dtype, st);
   return e == cudaSuccess ? DROPKV_OK : cuda_fail(e);
 }

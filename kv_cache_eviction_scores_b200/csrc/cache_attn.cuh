@@ -30,7 +30,6 @@ struct AttnDev {
   const int32_t* lengths;
   const int32_t* q_lengths;
   float* part;      // [2 grid][rows][pstride]
-  int4* desc;       // [grid][2]: the cut unit that begins in a CTA
   int32_t pstride;  // floats of a partial row: O (d rounded up to 4), m, l, pad
   int32_t* status;
 };
@@ -83,16 +82,16 @@ struct AttnPlanShared {
   int item, nt;
 };
 
-// The range of this CTA (kThreads threads, all call it).  total and grid: all
-// tiles and the CTAs that have a range (every one of them a non-empty one).
-template <int kRows, int kTile, int kThreads>
-__device__ __forceinline__ bool attn_plan(const AttnDev& a, AttnPlanShared& sh, AttnWalk& w,
-                                          int64_t& total, int& grid) {
+// The unit of one tile of the work (kThreads threads, all call it): pick(total)
+// names the tile, < 0 for none (then false).  Sets w but for left and t1.
+template <int kRows, int kTile, int kThreads, typename Pick>
+__device__ __forceinline__ bool attn_seek(const AttnDev& a, AttnPlanShared& sh, AttnWalk& w,
+                                          int64_t& total, Pick pick) {
   constexpr int kWarps = kThreads / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int items = a.c.B * a.nrt;
   // pass 1: all tiles; with no more items than threads its scan also places
-  // the range
+  // the tile
   int64_t sum = 0, incl = 0, base = 0;
   int mine = 0;
   for (int i0 = 0; i0 < items; i0 += kThreads) {
@@ -113,19 +112,18 @@ __device__ __forceinline__ bool attn_plan(const AttnDev& a, AttnPlanShared& sh, 
     if (i == warp) base = total;
     total += sh.warp_sum[i];
   }
-  grid = (int)min((int64_t)gridDim.x, total);
-  if ((int)blockIdx.x >= grid) return false;
-  const int64_t first = total * blockIdx.x / grid, last = total * (blockIdx.x + 1) / grid;
+  const int64_t at = pick(total);
+  if (at < 0) return false;
   if (items <= kThreads) {
     const int64_t e = base + incl - sum;  // tiles before this thread's item
-    if (first >= e && first < e + sum) {
+    if (at >= e && at < e + sum) {
       sh.item = threadIdx.x;
       sh.nt = mine;
       sh.g0 = e;
     }
     __syncthreads();
   } else {
-    // pass 2: the same scan chunk by chunk until the range's first tile
+    // pass 2: the same scan chunk by chunk until the tile
     int64_t before = 0;
     for (int i0 = 0; i0 < items; i0 += kThreads) {
       const int it = i0 + (int)threadIdx.x;
@@ -146,22 +144,46 @@ __device__ __forceinline__ bool attn_plan(const AttnDev& a, AttnPlanShared& sh, 
         all += sh.warp_sum[i];
       }
       const int64_t e = before + wb + s - own;
-      if (first >= e && first < e + own) {
+      if (at >= e && at < e + own) {
         sh.item = it;
         sh.nt = nt;
         sh.g0 = e;
       }
       before += all;
-      if (first < before) break;  // the same for every thread
+      if (at < before) break;  // the same for every thread
     }
     __syncthreads();
   }
   w.item = sh.item;
   w.nt = sh.nt;
-  const int64_t in_item = first - sh.g0;
+  const int64_t in_item = at - sh.g0;
   w.h = (int)(in_item / w.nt);
   w.t0 = (int)(in_item - (int64_t)w.h * w.nt);
   w.g0 = sh.g0 + (int64_t)w.h * w.nt;
+  return true;
+}
+
+// CTAs that have a range (every one of them a non-empty one), of `ctas`, and
+// the ranges' ends.
+__device__ __forceinline__ int attn_grid(int64_t total, int ctas) {
+  return (int)min((int64_t)ctas, total);
+}
+__device__ __forceinline__ int64_t attn_range(int64_t total, int grid, int cta) {
+  return total * cta / grid;
+}
+
+// The range of this CTA (kThreads threads, all call it).
+template <int kRows, int kTile, int kThreads>
+__device__ __forceinline__ bool attn_plan(const AttnDev& a, AttnPlanShared& sh, AttnWalk& w) {
+  int64_t total, first = 0, last = 0;
+  const bool some = attn_seek<kRows, kTile, kThreads>(a, sh, w, total, [&](int64_t all) -> int64_t {
+    const int grid = attn_grid(all, gridDim.x);
+    if ((int)blockIdx.x >= grid) return -1;
+    first = attn_range(all, grid, blockIdx.x);
+    last = attn_range(all, grid, blockIdx.x + 1);
+    return first;
+  });
+  if (!some) return false;
   w.left = last - first;
   w.t1 = (int)min((int64_t)w.nt, w.t0 + w.left);
   return true;
@@ -192,14 +214,6 @@ __device__ __forceinline__ int attn_slot(const AttnWalk& w) {
   if (w.t0 == 0 && w.t1 == w.nt) return -1;
   return 2 * (int)blockIdx.x + (w.t0 == 0 ? 1 : 0);
 }
-// Records the cut unit that begins in this CTA for the merge (one thread).
-__device__ __forceinline__ void attn_describe(const AttnDev& a, const AttnWalk& w, int64_t total,
-                                              int grid) {
-  const int64_t end = w.g0 + w.nt - 1;
-  const int c1 = (int)(((end + 1) * grid - 1) / total);  // the CTA of its last tile
-  a.desc[blockIdx.x] = make_int4(w.item, w.h, c1, 0);
-}
-
 // A row's output position.
 struct AttnRow {
   int b, hq, t;
@@ -218,16 +232,18 @@ __device__ __forceinline__ void attn_put_lse(const AttnDev& a, const AttnRow& x,
 }
 
 struct AttnGrid {
-  int ctas;
-  int rows;
+  int ctas, rows, tile;  // of a unit
 };
 // Grid and unit rows of each kernel (host); launchers of one call's kernels.
 AttnGrid attn_grid_simt();
 AttnGrid attn_grid_rows();
+AttnGrid attn_grid_few(int page_dtype);
 AttnGrid attn_grid_tile(bool alt);
 cudaError_t launch_attn_simt(const AttnDev& a, int page_dtype, int q_dtype, cudaStream_t st);
 cudaError_t launch_attn_rows(const AttnDev& a, int page_dtype, cudaStream_t st);
+cudaError_t launch_attn_few(const AttnDev& a, int page_dtype, cudaStream_t st);
 cudaError_t launch_attn_tile(const AttnDev& a, int page_dtype, bool alt, cudaStream_t st);
-cudaError_t launch_attn_merge(const AttnDev& a, int ctas, int rows, int q_dtype, cudaStream_t st);
+// The join of the units that the kernel of this grid cut.
+cudaError_t launch_attn_merge(const AttnDev& a, AttnGrid g, int q_dtype, cudaStream_t st);
 
 }  // namespace dropkv

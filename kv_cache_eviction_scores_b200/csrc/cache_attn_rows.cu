@@ -26,7 +26,7 @@ namespace dropkv {
 namespace {
 
 constexpr int kRRows = 16, kRWarps = 8, kRThreads = 32 * kRWarps, kRTile = 16 * kRWarps;
-constexpr int kRCtas = 148;
+constexpr int kRCtas = 148, kFRows = 8;
 
 template <typename TP>
 constexpr int ring_depth() {
@@ -68,15 +68,11 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t* a, uint3
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Two e4m3 bytes in bits 15..8 and 31..24 of x to a bf16 pair: sign, then the
-// seven bits moved to the bottom of bf16's exponent and the top of its
-// mantissa (subnormals land on subnormals), times 2^120 = 2^(127 - 7).  The NaN
-// code becomes 480; a stored NaN row carries it in its scale.
+// Two e4m3 bytes of x to a bf16 pair (the NaN code becomes 480; a stored NaN row
+// carries it in its scale).
+template <uint32_t kSel>
 __device__ __forceinline__ uint32_t widen2(uint32_t x) {
-  const uint32_t y = ((x >> 4) & 0x07F007F0u) | (x & 0x80008000u);
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(y), "r"(0x7B807B80u));
-  return r;
+  return widen_e4m3x2<kSel>(x, 0x7B807B80u);  // 2^120
 }
 
 // Byte offset of 16-byte piece `c` of row `row` in a swizzled tile of rows of
@@ -98,6 +94,46 @@ struct RowsShared {
   static constexpr int kBytes = kRing > kJoin ? kRing : kJoin;
 };
 
+// A unit's rows from its warps' scaled O (all: [warp][kRows][D + 4]) and (m, l):
+// to the output, or to the cut unit's partial.
+template <int D, int kRows>
+__device__ __forceinline__ void put_joined(const AttnDev& a, const AttnWalk& w, int b, int rt,
+                                           int rows, const float2 (&sml)[kRWarps][kRows],
+                                           const float* all) {
+  const int slot = attn_slot(w);
+  for (int i = threadIdx.x; i < rows * (D / 4); i += kRThreads) {
+    const int r = i / (D / 4), c = i % (D / 4) * 4;
+    float M = -CUDART_INF_F;
+#pragma unroll
+    for (int k = 0; k < kRWarps; ++k) M = fmaxf(M, sml[k][r].x);
+    float l = 0.f;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kRWarps; ++k) {
+      const float2 ml = sml[k][r];
+      l += ml.x == -CUDART_INF_F ? ml.y : ml.y * attn_ex2(ml.x - M);
+      const float4 z = *reinterpret_cast<const float4*>(all + (k * kRows + r) * (D + 4) + c);
+      y.x += z.x;
+      y.y += z.y;
+      y.z += z.z;
+      y.w += z.w;
+    }
+    if (slot < 0) {
+      const AttnRow x = attn_row(a, b, w.h, rt * kRows + r);
+      __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) + x.b * a.os[0] +
+                           x.hq * a.os[1] + x.t * a.os[2];
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      *reinterpret_cast<uint2*>(out + c) =
+          make_uint2(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
+      if (c == 0) attn_put_lse(a, x, M, l);
+    } else {
+      float* out = a.part + ((size_t)slot * kRows + r) * a.pstride;
+      *reinterpret_cast<float4*>(out + c) = y;
+      if (c == 0) *reinterpret_cast<float2*>(out + a.pstride - 4) = make_float2(M, l);
+    }
+  }
+}
+
 template <typename TP, int D>
 __global__ void __launch_bounds__(kRThreads, 1) k_attn_rows(const AttnDev a) {
   using S = RowsShared<TP, D>;
@@ -117,11 +153,8 @@ __global__ void __launch_bounds__(kRThreads, 1) k_attn_rows(const AttnDev a) {
   const uint32_t ring_s = smem_addr(ring);
   const uint8_t* kp = reinterpret_cast<const uint8_t*>(a.c.k);
   const uint8_t* vp = reinterpret_cast<const uint8_t*>(a.c.v);
-  int64_t total;
-  int grid;
   AttnWalk w;
-  bool more = attn_plan<kRRows, kRTile, kRThreads>(a, plan, w, total, grid);
-  bool described = false;
+  bool more = attn_plan<kRRows, kRTile, kRThreads>(a, plan, w);
   while (more) {
     const int b = w.item / a.nrt, rt = w.item - b * a.nrt;
     int L, n;
@@ -187,14 +220,14 @@ __global__ void __launch_bounds__(kRThreads, 1) k_attn_rows(const AttnDev a) {
       for (int ks = 0; ks < D / 16; ++ks) {
         if constexpr (kScaled) {
           // the product's k order follows the widened bytes: k = 2t, 2t+1 are
-          // dims 4t, 4t+2, and k = 2t+8, 2t+9 dims 4t+1, 4t+3 of the 16
+          // dims 4t, 4t+1, and k = 2t+8, 2t+9 dims 4t+2, 4t+3 of the 16
           uint2 u0 = make_uint2(0, 0), u1 = u0;
           if (live0) u0 = *reinterpret_cast<const uint2*>(q0 + ks * 16 + 4 * tq);
           if (live1) u1 = *reinterpret_cast<const uint2*>(q1 + ks * 16 + 4 * tq);
-          qa[ks][0] = __byte_perm(u0.x, u0.y, 0x5410);
-          qa[ks][2] = __byte_perm(u0.x, u0.y, 0x7632);
-          qa[ks][1] = __byte_perm(u1.x, u1.y, 0x5410);
-          qa[ks][3] = __byte_perm(u1.x, u1.y, 0x7632);
+          qa[ks][0] = u0.x;
+          qa[ks][2] = u0.y;
+          qa[ks][1] = u1.x;
+          qa[ks][3] = u1.y;
         } else {
           const uint32_t* p0 = reinterpret_cast<const uint32_t*>(q0 + ks * 16 + 2 * tq);
           const uint32_t* p1 = reinterpret_cast<const uint32_t*>(q1 + ks * 16 + 2 * tq);
@@ -250,7 +283,7 @@ __global__ void __launch_bounds__(kRThreads, 1) k_attn_rows(const AttnDev a) {
             ldsm4(r, tk + swz<kPieces>((mi & 1) * 8 + mr, c + (mi >> 1)));
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-              mma16816(s[u & 1], qa[c + (u >> 1)], widen2(r[u] << 8), widen2(r[u]));
+              mma16816(s[u & 1], qa[c + (u >> 1)], widen2<kBytes01>(r[u]), widen2<kBytes23>(r[u]));
           }
         } else {
 #pragma unroll
@@ -361,8 +394,8 @@ __global__ void __launch_bounds__(kRThreads, 1) k_attn_rows(const AttnDev a) {
               ldsm4t(r, tv + swz<kPieces>((mi & 1) * 8 + mr, c + (mi >> 1)));
 #pragma unroll
               for (int u = 0; u < 2; ++u) {  // even dims of the piece, then the odd ones
-                mma16816(o[2 * (c + u)], pa, widen2(r[2 * u] << 8), widen2(r[2 * u + 1] << 8));
-                mma16816(o[2 * (c + u) + 1], pa, widen2(r[2 * u]), widen2(r[2 * u + 1]));
+                mma16816(o[2 * (c + u)], pa, widen2<kBytes02>(r[2 * u]), widen2<kBytes02>(r[2 * u + 1]));
+                mma16816(o[2 * (c + u) + 1], pa, widen2<kBytes13>(r[2 * u]), widen2<kBytes13>(r[2 * u + 1]));
               }
             }
           } else {
@@ -454,68 +487,406 @@ __global__ void __launch_bounds__(kRThreads, 1) k_attn_rows(const AttnDev a) {
       }
     }
     __syncthreads();
-    const int slot = attn_slot(w);
-    const float* all = reinterpret_cast<const float*>(sm);
-    for (int i = threadIdx.x; i < rows * (D / 4); i += kRThreads) {
-      const int r = i / (D / 4), c = i % (D / 4) * 4;
-      float M = -CUDART_INF_F;
-#pragma unroll
-      for (int k = 0; k < kRWarps; ++k) M = fmaxf(M, sml[k][r].x);
-      float l = 0.f;
-      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int k = 0; k < kRWarps; ++k) {
-        const float2 ml = sml[k][r];
-        l += ml.x == -CUDART_INF_F ? ml.y : ml.y * attn_ex2(ml.x - M);
-        const float4 z = *reinterpret_cast<const float4*>(all + (k * kRRows + r) * (D + 4) + c);
-        y.x += z.x;
-        y.y += z.y;
-        y.z += z.z;
-        y.w += z.w;
-      }
-      if (slot < 0) {
-        const AttnRow x = attn_row(a, b, w.h, rt * kRRows + r);
-        __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) + x.b * a.os[0] +
-                             x.hq * a.os[1] + x.t * a.os[2];
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        *reinterpret_cast<uint2*>(out + c) =
-            make_uint2(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
-        if (c == 0) attn_put_lse(a, x, M, l);
-      } else {
-        float* out = a.part + ((size_t)slot * kRRows + r) * a.pstride;
-        *reinterpret_cast<float4*>(out + c) = y;
-        if (c == 0) *reinterpret_cast<float2*>(out + a.pstride - 4) = make_float2(M, l);
-      }
-    }
-    if (slot >= 0 && (slot & 1)) {
-      if (threadIdx.x == 0) attn_describe(a, w, total, grid);
-      described = true;
-    }
+    put_joined<D, kRRows>(a, w, b, rt, rows, sml, reinterpret_cast<const float*>(sm));
     more = attn_next<kRRows, kRTile>(a, w);
     if (more) __syncthreads();  // the joined rows are read out
   }
-  if (!described && threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+}
+
+// ---- up to eight rows per KV head -------------------------------------------------
+//
+// The products the other way round: S^T = K Q^T with 16 slots as the rows of
+// m16n8k16 and the (at most eight) query rows as its columns, and O^T = V^T P^T
+// with 16 dims as rows.  Half the matrix instructions and half the registers of
+// the kernel above, whose row block would be half empty; with e4m3 pages, whose
+// tiles are half the bytes, two CTAs then fit an SM, and their warps hide each
+// other's latencies, which bound that kernel there (64 sequences of 2K to 16K
+// e4m3 slots, 7 rows each: MEASURE_FEW).
+template <typename TP, int D>
+struct FewShared {
+  static constexpr int kDepth = 3;
+  static constexpr int kRowBytes = D * (int)sizeof(TP);
+  static constexpr int kHalf = 16 * kRowBytes;  // K or V of 16 slots
+  static constexpr int kRing = kRWarps * kDepth * 2 * kHalf;
+  static constexpr int kJoin = kRWarps * kFRows * (D + 4) * 4;
+  static constexpr int kBytes = kRing > kJoin ? kRing : kJoin;
+};
+
+template <typename TP>
+constexpr int few_ctas_per_sm() {
+  return sizeof(TP) == 1 ? 2 : 1;
+}
+
+// Transposes an 8 x 8 matrix of 16-bit values held by a warp as ldmatrix leaves it.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+template <typename TP, int D>
+__global__ void __launch_bounds__(kRThreads, few_ctas_per_sm<TP>()) k_attn_few(const AttnDev a) {
+  using S = FewShared<TP, D>;
+  constexpr int kDepth = S::kDepth;
+  constexpr bool kScaled = sizeof(TP) == 1;
+  constexpr int kPieces = S::kRowBytes / 16;
+  constexpr int kPerPass = 32 / kPieces;  // rows a warp copies at once
+  extern __shared__ __align__(128) uint8_t sm[];
+  __shared__ AttnPlanShared plan;
+  __shared__ int srow[kRWarps][kDepth][16];    // pool rows of the ring's slots, -1: none
+  __shared__ float sscale[kRWarps][2][2][16];  // K's scale times c_log2, V's scale
+  __shared__ float2 sml[kRWarps][kFRows];
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, tq = lane & 3;
+  uint8_t* ring = sm + warp * kDepth * 2 * S::kHalf;
+  const uint32_t ring_s = smem_addr(ring);
+  const uint8_t* kp = reinterpret_cast<const uint8_t*>(a.c.k);
+  const uint8_t* vp = reinterpret_cast<const uint8_t*>(a.c.v);
+  AttnWalk w;
+  bool more = attn_plan<kFRows, kRTile, kRThreads>(a, plan, w);
+  while (more) {
+    const int b = w.item / a.nrt, rt = w.item - b * a.nrt;
+    int L, n;
+    attn_lengths(a, b, L, n);
+    const int rows = min(kFRows, a.G * n - rt * kFRows);
+    const int seen_all = attn_seen(a, L, n, rt * kFRows + rows - 1);
+    const int seen_min = attn_seen(a, L, n, rt * kFRows);
+    const int32_t* table = a.c.table + (size_t)b * a.c.max_pages;
+
+    // the page of this lane's slot (lane & 15) of tile t: looked up one step
+    // before its copy is issued (volatile: requested here)
+    int npage = -1, noff = -1;
+    auto look = [&](int t) {
+      const int slot = t * kRTile + warp * 16 + (lane & 15);
+      npage = noff = -1;
+      if (t < w.t1 && slot < seen_all) {
+        const int pi = (int)a.c.fpage.div((uint32_t)slot);
+        asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(npage) : "l"(table + pi));
+        noff = slot - pi * a.c.page;
+      }
+    };
+    auto issue = [&](int st) {
+      int row = -1;
+      if ((uint32_t)npage < (uint32_t)a.c.n_pages)
+        row = (npage * a.c.Hkv + w.h) * a.c.page + noff;
+      else if (noff >= 0)
+        raise_arg(a.status);
+      if (lane < 16) srow[warp][st][lane] = row;
+      const uint32_t dk = ring_s + st * 2 * S::kHalf, dv = dk + S::kHalf;
+      const int c = lane % kPieces;
+#pragma unroll
+      for (int i = 0; i < 16 / kPerPass; ++i) {
+        const int r = lane / kPieces + i * kPerPass;
+        const int at = __shfl_sync(0xffffffffu, row, r);
+        const size_t off = at < 0 ? 0 : (size_t)at * S::kRowBytes + c * 16;
+        copy16(dk + swz<kPieces>(r, c), kp + off, at >= 0);
+        copy16(dv + swz<kPieces>(r, c), vp + off, at >= 0);
+      }
+    };
+    look(w.t0);
+#pragma unroll
+    for (int i = 0; i < kDepth - 1; ++i) {
+      issue(i);
+      copy_commit();
+      look(w.t0 + i + 1);
+    }
+
+    // query row g as a B fragment (k: dims, n: rows), and the two rows whose
+    // logits this lane holds
+    uint32_t qb[D / 16][2];
+    {
+      const bool on = g < rows;
+      const AttnRow x = attn_row(a, b, w.h, rt * kFRows + (on ? g : 0));
+      const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) + x.b * a.qs[0] +
+                               x.hq * a.qs[1] + x.t * a.qs[2];
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        if constexpr (kScaled) {
+          // k in the order of the widened bytes: 2t, 2t+1 are dims 4t, 4t+1, and
+          // 2t+8, 2t+9 dims 4t+2, 4t+3 of the 16
+          const uint2 u = on ? *reinterpret_cast<const uint2*>(q + ks * 16 + 4 * tq) : make_uint2(0, 0);
+          qb[ks][0] = u.x;
+          qb[ks][1] = u.y;
+        } else {
+          const uint32_t* p = reinterpret_cast<const uint32_t*>(q + ks * 16 + 2 * tq);
+          qb[ks][0] = on ? p[0] : 0u;
+          qb[ks][1] = on ? p[4] : 0u;
+        }
+      }
+    }
+    const int q0 = 2 * tq, q1 = q0 + 1;
+    const int seen0 = q0 < rows ? attn_seen(a, L, n, rt * kFRows + q0) : 0;
+    const int seen1 = q1 < rows ? attn_seen(a, L, n, rt * kFRows + q1) : 0;
+    float m0 = -CUDART_INF_F, m1 = -CUDART_INF_F, l0 = 0.f, l1 = 0.f;
+    float o[D / 16][4];  // dims g, g + 8 (e4m3: 2 g, 2 g + 1) of each 16; rows q0, q1
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[i][k] = 0.f;
+
+    // scale bytes of the first tile (lanes 0..15 K's, 16..31 V's)
+    uint32_t sbyte = 0;
+    auto scale_load = [&](int st) {
+      const int row = srow[warp][st][lane & 15];
+      sbyte = 0;
+      if (row >= 0)
+        asm volatile("ld.global.nc.u8 %0, [%1];"
+                     : "=r"(sbyte)
+                     : "l"((lane < 16 ? a.c.ks : a.c.vs) + row));
+    };
+    __syncwarp();
+    if (kScaled) scale_load(0);
+
+    int st = 0;
+    for (int t = w.t0; t < w.t1; ++t) {
+      copy_wait<kDepth - 2>();
+      __syncwarp();  // the tile has landed for every lane, and the last one is read out
+      const uint32_t valid = __ballot_sync(0xffffffffu, srow[warp][st][lane & 15] >= 0) & 0xFFFFu;
+      const int base = t * kRTile + warp * 16;
+      if (kScaled)
+        sscale[warp][t & 1][lane >> 4][lane & 15] = scale_of(sbyte) * (lane < 16 ? a.c_log2 : 1.f);
+      const int stn = st + kDepth - 1 >= kDepth ? st - 1 : st + kDepth - 1;
+      issue(stn);
+      copy_commit();
+      look(t + kDepth);
+      __syncwarp();
+      const int st1 = st + 1 == kDepth ? 0 : st + 1;
+      if (kScaled && t + 1 < w.t1) scale_load(st1);
+      const uint32_t tk = ring_s + st * 2 * S::kHalf, tv = tk + S::kHalf;
+      if (valid) {  // some slot of the 16 is there
+        const int mi = lane >> 3, mr = lane & 7;  // ldmatrix: matrix and row of this lane
+        // S^T of slots g (s[0], s[1]) and g + 8 (s[2], s[3]) for rows q0, q1
+        float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
+        if constexpr (kScaled) {
+#pragma unroll
+          for (int c = 0; c < D / 16; c += 2) {
+            uint32_t r[4];  // slots 0-7 and 8-15 of piece c, then of piece c + 1
+            ldsm4(r, tk + swz<kPieces>((mi & 1) * 8 + mr, c + (mi >> 1)));
+            const uint32_t ka[4] = {widen2<kBytes01>(r[0]), widen2<kBytes01>(r[1]),
+                                    widen2<kBytes23>(r[0]), widen2<kBytes23>(r[1])};
+            const uint32_t kb[4] = {widen2<kBytes01>(r[2]), widen2<kBytes01>(r[3]),
+                                    widen2<kBytes23>(r[2]), widen2<kBytes23>(r[3])};
+            mma16816(s, ka, qb[c][0], qb[c][1]);
+            mma16816(s2, kb, qb[c + 1][0], qb[c + 1][1]);
+          }
+        } else {
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ks += 2) {
+            uint32_t r[4], r2[4];
+            ldsm4(r, tk + swz<kPieces>((mi & 1) * 8 + mr, ks * 2 + (mi >> 1)));
+            ldsm4(r2, tk + swz<kPieces>((mi & 1) * 8 + mr, ks * 2 + 2 + (mi >> 1)));
+            mma16816(s, r, qb[ks][0], qb[ks][1]);
+            mma16816(s2, r2, qb[ks + 1][0], qb[ks + 1][1]);
+          }
+        }
+        float kf0 = a.c_log2, kf1 = a.c_log2, vf0 = 1.f, vf1 = 1.f;  // slots g, g + 8
+        if (kScaled) {
+          kf0 = sscale[warp][t & 1][0][g];
+          kf1 = sscale[warp][t & 1][0][g + 8];
+          vf0 = sscale[warp][t & 1][1][g];
+          vf1 = sscale[warp][t & 1][1][g + 8];
+        }
+        s[0] = (s[0] + s2[0]) * kf0;
+        s[1] = (s[1] + s2[1]) * kf0;
+        s[2] = (s[2] + s2[2]) * kf1;
+        s[3] = (s[3] + s2[3]) * kf1;
+        // slots that some row of the unit does not see
+        const bool partly = valid != 0xFFFFu || base + 16 > seen_min;
+        uint32_t hid = 0;  // bit e: s[e] is hidden
+        if (partly) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = g + 8 * (e >> 1);
+            if (base + j >= (e & 1 ? seen1 : seen0) || !((valid >> j) & 1)) {
+              hid |= 1u << e;
+              s[e] = -CUDART_INF_F;
+            }
+          }
+        }
+        float t0 = fmaxf(s[0], s[2]), t1 = fmaxf(s[1], s[3]);
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) {
+          t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, x));
+          t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, x));
+        }
+        if (__any_sync(0xffffffffu, t0 > m0 + 8.f || t1 > m1 + 8.f)) {
+          const float n0 = t0 > m0 + 8.f ? t0 : m0, n1 = t1 > m1 + 8.f ? t1 : m1;
+          const float f0 = m0 == -CUDART_INF_F ? 0.f : attn_ex2(m0 - n0);
+          const float f1 = m1 == -CUDART_INF_F ? 0.f : attn_ex2(m1 - n1);
+          m0 = n0;
+          m1 = n1;
+          l0 *= f0;
+          l1 *= f1;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            o[i][0] *= f0;
+            o[i][1] *= f1;
+            o[i][2] *= f0;
+            o[i][3] *= f1;
+          }
+        }
+        const float u0 = m0 == -CUDART_INF_F ? 0.f : m0, u1 = m1 == -CUDART_INF_F ? 0.f : m1;
+        float p[4] = {attn_ex2(s[0] - u0), attn_ex2(s[1] - u1), attn_ex2(s[2] - u0),
+                      attn_ex2(s[3] - u1)};
+        l0 += p[0] + p[2];
+        l1 += p[1] + p[3];
+        if (kScaled) {
+          p[0] *= vf0;
+          p[1] *= vf0;
+          p[2] *= vf1;
+          p[3] *= vf1;
+          if (partly) {  // a NaN scale of a hidden slot
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if ((hid >> e) & 1) p[e] = 0.f;
+          }
+        }
+        // P^T as a B fragment (k: slots, n: rows)
+        const uint32_t pb0 = transpose8(pack_bf16(p[0], p[1]));
+        const uint32_t pb1 = transpose8(pack_bf16(p[2], p[3]));
+        bool odd = false;  // a hidden slot's V may be an infinity or a NaN
+        if (!kScaled && partly) {
+          const int c = lane % kPieces;
+#pragma unroll
+          for (int i = 0; i < 16 / kPerPass; ++i) {
+            const uint4 v = *reinterpret_cast<const uint4*>(
+                ring + st * 2 * S::kHalf + S::kHalf + swz<kPieces>(lane / kPieces + i * kPerPass, c));
+            const uint32_t y[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              odd = odd || (y[k] & 0x7F80u) == 0x7F80u || (y[k] & 0x7F800000u) == 0x7F800000u;
+          }
+          odd = __any_sync(0xffffffffu, odd);
+        }
+        if (!odd) {
+          if constexpr (kScaled) {
+#pragma unroll
+            for (int c = 0; c < D / 16; c += 2) {
+              uint32_t r[4];  // slots 0-7 and 8-15 of piece c, then of piece c + 1
+              ldsm4t(r, tv + swz<kPieces>((mi & 1) * 8 + mr, c + (mi >> 1)));
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const uint32_t va[4] = {widen2<kBytes02>(r[2 * u]), widen2<kBytes13>(r[2 * u]),
+                                        widen2<kBytes02>(r[2 * u + 1]), widen2<kBytes13>(r[2 * u + 1])};
+                mma16816(o[c + u], va, pb0, pb1);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t r[4];  // dims 0-7 and 8-15 of slots 0-7, then of slots 8-15
+              ldsm4t(r, tv + swz<kPieces>((mi >> 1) * 8 + mr, 2 * c + (mi & 1)));
+              mma16816(o[c], r, pb0, pb1);
+            }
+          }
+        } else {
+          // out of the ordinary: 0 * NaN must not reach the rows that do not
+          // see the slot, so P V by scalars over the slots that a row sees
+#pragma unroll 1
+          for (int j = 0; j < 16; ++j) {
+            const int from = (j & 7) * 4 + tq;
+            const float w0 = __shfl_sync(0xffffffffu, j < 8 ? p[0] : p[2], from);
+            const float w1 = __shfl_sync(0xffffffffu, j < 8 ? p[1] : p[3], from);
+            const uint32_t h = __shfl_sync(0xffffffffu, j < 8 ? hid : hid >> 2, from);
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint16_t v = *reinterpret_cast<const uint16_t*>(
+                    ring + st * 2 * S::kHalf + S::kHalf + swz<kPieces>(j, (2 * c + e) % kPieces) + 2 * g);
+                const float x = __uint_as_float((uint32_t)v << 16);
+                if (!(h & 1)) o[c][2 * e] = fmaf(w0, x, o[c][2 * e]);
+                if (!(h & 2)) o[c][2 * e + 1] = fmaf(w1, x, o[c][2 * e + 1]);
+              }
+          }
+        }
+      }
+      st = st1;
+    }
+    copy_wait<0>();
+
+    // join the warps: row maxima and sums, then the scaled O
+#pragma unroll
+    for (int x = 4; x < 32; x <<= 1) {
+      l0 += __shfl_xor_sync(0xffffffffu, l0, x);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, x);
+    }
+    if (g == 0) {
+      sml[warp][q0] = make_float2(m0, l0);
+      sml[warp][q1] = make_float2(m1, l1);
+    }
+    __syncthreads();  // every warp's ring is read out, too
+    float M0 = -CUDART_INF_F, M1 = -CUDART_INF_F;
+#pragma unroll
+    for (int i = 0; i < kRWarps; ++i) {
+      M0 = fmaxf(M0, sml[i][q0].x);
+      M1 = fmaxf(M1, sml[i][q1].x);
+    }
+    const float f0 = m0 == -CUDART_INF_F ? (l0 == 0.f ? 0.f : l0) : attn_ex2(m0 - M0);
+    const float f1 = m1 == -CUDART_INF_F ? (l1 == 0.f ? 0.f : l1) : attn_ex2(m1 - M1);
+    float* join = reinterpret_cast<float*>(sm) + warp * kFRows * (D + 4);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if ((e ? q1 : q0) >= rows) continue;
+      float* to = join + (e ? q1 : q0) * (D + 4);
+      const float f = e ? f1 : f0;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        if constexpr (kScaled) {
+          *reinterpret_cast<float2*>(to + c * 16 + 2 * g) = make_float2(o[c][e] * f, o[c][2 + e] * f);
+        } else {
+          to[c * 16 + g] = o[c][e] * f;
+          to[c * 16 + 8 + g] = o[c][2 + e] * f;
+        }
+      }
+    }
+    __syncthreads();
+    put_joined<D, kFRows>(a, w, b, rt, rows, sml, reinterpret_cast<const float*>(sm));
+    more = attn_next<kFRows, kRTile>(a, w);
+    if (more) __syncthreads();  // the joined rows are read out
+  }
 }
 
 template <typename TP, int D>
 cudaError_t launch_rows(const AttnDev& a, cudaStream_t st) {
   const auto kern = k_attn_rows<TP, D>;
   constexpr int smem = RowsShared<TP, D>::kBytes;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = allow_smem<k_attn_rows<TP, D>>(smem);
   if (e != cudaSuccess) return e;
   kern<<<kRCtas, kRThreads, smem, st>>>(a);
   return cudaGetLastError();
 }
 
+template <typename TP, int D>
+cudaError_t launch_few(const AttnDev& a, cudaStream_t st) {
+  constexpr int smem = FewShared<TP, D>::kBytes;
+  cudaError_t e = allow_smem<k_attn_few<TP, D>>(smem);
+  if (e != cudaSuccess) return e;
+  k_attn_few<TP, D><<<kRCtas * few_ctas_per_sm<TP>(), kRThreads, smem, st>>>(a);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
-AttnGrid attn_grid_rows() { return {kRCtas, kRRows}; }
+AttnGrid attn_grid_rows() { return {kRCtas, kRRows, kRTile}; }
+AttnGrid attn_grid_few(int page_dtype) {
+  const int per = page_dtype == DROPKV_E4M3 ? few_ctas_per_sm<E4M3>() : few_ctas_per_sm<__nv_bfloat16>();
+  return {kRCtas * per, kFRows, kRTile};
+}
 
 cudaError_t launch_attn_rows(const AttnDev& a, int page_dtype, cudaStream_t st) {
   if (page_dtype == DROPKV_BF16)
     return a.c.d == 128 ? launch_rows<__nv_bfloat16, 128>(a, st)
                         : launch_rows<__nv_bfloat16, 64>(a, st);
   return a.c.d == 128 ? launch_rows<E4M3, 128>(a, st) : launch_rows<E4M3, 64>(a, st);
+}
+
+cudaError_t launch_attn_few(const AttnDev& a, int page_dtype, cudaStream_t st) {
+  if (page_dtype == DROPKV_BF16)
+    return a.c.d == 128 ? launch_few<__nv_bfloat16, 128>(a, st)
+                        : launch_few<__nv_bfloat16, 64>(a, st);
+  return a.c.d == 128 ? launch_few<E4M3, 128>(a, st) : launch_few<E4M3, 64>(a, st);
 }
 
 }  // namespace dropkv

@@ -18,16 +18,6 @@ namespace {
 constexpr int kSRows = 16, kSTile = 32, kSThreads = 128, kSCtas = 592;  // four CTAs an SM
 
 __device__ __forceinline__ float4 four(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 four(const __nv_bfloat16* p) {
-  const uint2 w = *reinterpret_cast<const uint2*>(p);
-  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
-                     __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u));
-}
-__device__ __forceinline__ float4 four(const E4M3* p) {
-  const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
-  const float2 a = unpack_e4m3(w & 0xFFFFu), b = unpack_e4m3(w >> 16);
-  return make_float4(a.x, a.y, b.x, b.y);
-}
 __device__ __forceinline__ float single(const float* p) { return *p; }
 __device__ __forceinline__ float single(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 __device__ __forceinline__ float single(const E4M3* p) { return unpack_e4m3(p->bits).x; }
@@ -37,23 +27,84 @@ __device__ __forceinline__ void store_out(__nv_bfloat16* p, float x) { *p = __fl
 // Floats between rows in shared memory: d in whole float4s, an odd number of them.
 __host__ __device__ __forceinline__ int row_stride(int d) { return (((d + 3) / 4) | 1) * 4; }
 
-// One pool row (or zeros) to fp32 in shared memory, by one warp.
+// Four values as they are stored.
 template <typename TP>
-__device__ __forceinline__ void widen_row(float* dst, const TP* pool, int64_t row, float f, int d,
-                                          int lane) {
-  const int d4 = (d + 3) & ~3;
-  if (row < 0) {
-    for (int i = lane; i < d4; i += 32) dst[i] = 0.f;
-    return;
+struct Four {};
+template <>
+struct Four<float> {
+  float4 w;
+  __device__ __forceinline__ float4 get() const { return w; }
+};
+template <>
+struct Four<__nv_bfloat16> {
+  uint2 w;
+  __device__ __forceinline__ float4 get() const {
+    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
+                       __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u));
   }
-  const TP* p = pool + row * d;
-  if ((d & 3) == 0) {
+};
+template <>
+struct Four<E4M3> {
+  uint32_t w;
+  __device__ __forceinline__ float4 get() const {
+    const float2 a = unpack_e4m3(w & 0xFFFFu), b = unpack_e4m3(w >> 16);
+    return make_float4(a.x, a.y, b.x, b.y);
+  }
+};
+
+// The kSTile / 4 rows of K and of V that are this warp's, to fp32 in shared memory
+// (zeros where there is no row).  All of a column block's loads are in flight
+// together: one after the other, their latencies were most of the kernel's time.
+template <typename TP>
+__device__ __forceinline__ void widen_rows(const AttnDev& a, float* sK, float* sV, int ds,
+                                           const int64_t (&srow)[kSTile], int warp, int lane) {
+  constexpr int kMine = kSTile / 4;
+  const int d = a.c.d, d4 = (d + 3) & ~3;
+  const TP* pool[2] = {reinterpret_cast<const TP*>(a.c.k), reinterpret_cast<const TP*>(a.c.v)};
+  int64_t row[kMine];
+  float f[2][kMine];
+#pragma unroll
+  for (int j = 0; j < kMine; ++j) {
+    row[j] = srow[warp + 4 * j];
+    f[0][j] = f[1][j] = 1.f;
+    if (sizeof(TP) == 1 && row[j] >= 0) {
+      f[0][j] = scale_of(__ldg(a.c.ks + row[j]));
+      f[1][j] = scale_of(__ldg(a.c.vs + row[j]));
+    }
+  }
+  if (d % 4 == 0) {
     for (int i = lane * 4; i < d; i += 128) {
-      float4 x = four(p + i);
-      *reinterpret_cast<float4*>(dst + i) = make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
+      Four<TP> x[2][kMine];
+#pragma unroll
+      for (int v = 0; v < 2; ++v)
+#pragma unroll
+        for (int j = 0; j < kMine; ++j) {
+          x[v][j] = Four<TP>{};
+          if (row[j] >= 0) x[v][j] = *reinterpret_cast<const Four<TP>*>(pool[v] + row[j] * d + i);
+        }
+#pragma unroll
+      for (int v = 0; v < 2; ++v)
+#pragma unroll
+        for (int j = 0; j < kMine; ++j) {
+          const float4 y = x[v][j].get();
+          const float s = f[v][j];
+          *reinterpret_cast<float4*>((v ? sV : sK) + (warp + 4 * j) * ds + i) =
+              make_float4(y.x * s, y.y * s, y.z * s, y.w * s);
+        }
     }
   } else {
-    for (int i = lane; i < d4; i += 32) dst[i] = i < d ? single(p + i) * f : 0.f;
+    for (int i = lane; i < d4; i += 32) {
+      float x[2][kMine];
+#pragma unroll
+      for (int v = 0; v < 2; ++v)
+#pragma unroll
+        for (int j = 0; j < kMine; ++j)
+          x[v][j] = row[j] >= 0 && i < d ? single(pool[v] + row[j] * d + i) : 0.f;
+#pragma unroll
+      for (int v = 0; v < 2; ++v)
+#pragma unroll
+        for (int j = 0; j < kMine; ++j) (v ? sV : sK)[(warp + 4 * j) * ds + i] = x[v][j] * f[v][j];
+    }
   }
 }
 
@@ -69,11 +120,8 @@ __global__ void __launch_bounds__(kSThreads) k_attn_simt(const AttnDev a) {
   float* sV = sK + kSTile * ds;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float* sP = sV + kSTile * ds + warp * (kSTile * 4);  // this warp's [slot][4 rows]
-  int64_t total;
-  int grid;
   AttnWalk w;
-  bool more = attn_plan<kSRows, kSTile, kSThreads>(a, plan, w, total, grid);
-  bool described = false;
+  bool more = attn_plan<kSRows, kSTile, kSThreads>(a, plan, w);
   while (more) {
     const int b = w.item / a.nrt, rt = w.item - b * a.nrt;
     int L, n;
@@ -115,16 +163,7 @@ __global__ void __launch_bounds__(kSThreads) k_attn_simt(const AttnDev a) {
     }
     __syncthreads();
     for (int t = w.t0; t < w.t1; ++t) {
-      for (int j = warp; j < kSTile; j += 4) {
-        const int64_t row = srow[t & 1][j];
-        float fk = 1.f, fv = 1.f;
-        if (sizeof(TP) == 1 && row >= 0) {
-          fk = scale_of(a.c.ks[row]);
-          fv = scale_of(a.c.vs[row]);
-        }
-        widen_row(sK + j * ds, reinterpret_cast<const TP*>(a.c.k), row, fk, d, lane);
-        widen_row(sV + j * ds, reinterpret_cast<const TP*>(a.c.v), row, fv, d, lane);
-      }
+      widen_rows<TP>(a, sK, sV, ds, srow[t & 1], warp, lane);
       const bool absent = srow[t & 1][lane] < 0;
       if (warp == 0 && t + 1 < w.t1) place(t + 1);
       __syncthreads();
@@ -203,91 +242,172 @@ __global__ void __launch_bounds__(kSThreads) k_attn_simt(const AttnDev a) {
         if (lane == 0) *reinterpret_cast<float2*>(out + a.pstride - 4) = make_float2(m[k], l[k]);
       }
     }
-    if (slot >= 0 && (slot & 1)) {
-      if (threadIdx.x == 0) attn_describe(a, w, total, grid);
-      described = true;
-    }
     more = attn_next<kSRows, kSTile>(a, w);
   }
-  if (!described && threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
 }
 
 // Joins the partials of the cut unit that began in CTA blockIdx.x: a warp per
 // row, the pieces in the order of their slots:
 //   M = max m_i, l = sum l_i 2^(m_i - M), O = sum O_i 2^(m_i - M) / l.
-// Loads of up to four pieces are in flight.  A piece whose row saw nothing has
-// m = -inf and l = 0 and is left out (its O is 0).
-template <typename TQ>
-__global__ void __launch_bounds__(128) k_attn_merge(const AttnDev a, int unit_rows) {
-  pdl_wait();
-  const int4 de = a.desc[blockIdx.x];
-  if (de.x < 0) return;
+// A piece whose row saw nothing has m = -inf and l = 0 and is left out (its O is
+// 0).  Which unit and how many pieces follows from the lengths alone and is found
+// before the wait for the kernel that writes the partials; after it, the first
+// kFly pieces of O travel together with the (m, l) pairs.
+template <typename TQ, int kRows, int kTile>
+__global__ void __launch_bounds__(128) k_attn_merge(const AttnDev a, int ctas) {
+  constexpr int kFly = 12;
+  __shared__ AttnPlanShared plan;
+  AttnWalk w;
+  int64_t total, first = 0, last = 0;
+  int grid = 0;
+  const int c0 = (int)blockIdx.x;
+  const bool some = attn_seek<kRows, kTile, 128>(a, plan, w, total, [&](int64_t all) -> int64_t {
+    grid = attn_grid(all, ctas);
+    if (c0 >= grid) return -1;
+    first = attn_range(all, grid, c0);
+    last = attn_range(all, grid, c0 + 1);
+    return last - 1;
+  });
+  // the unit of the range's last tile, if it begins here and ends elsewhere
+  if (!some || w.g0 < first || w.g0 + w.nt <= last) {
+    pdl_wait();
+    return;
+  }
+  const int c1 = (int)(((w.g0 + w.nt) * grid - 1) / total);  // the CTA of its last tile
+  const int pieces = c1 - c0 + 1;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int b = de.x / a.nrt, rt = de.x - b * a.nrt;
+  const int b = w.item / a.nrt, rt = w.item - b * a.nrt;
   int L, n;
   attn_lengths(a, b, L, n);
-  const int rows = min(unit_rows, a.G * n - rt * unit_rows);
-  const int c0 = (int)blockIdx.x, pieces = de.z - c0 + 1;
+  const int rows = min(kRows, a.G * n - rt * kRows);
   const int d = a.c.d;
+  pdl_wait();
+  if (kRows > 16 && pieces <= 4) {
+    // large units are cut into few pieces: four rows at a time, lane 4 k + i with
+    // row k's (m, l) of piece i
+    for (int r0 = (blockIdx.y * 4 + warp) * 4; r0 < rows; r0 += gridDim.y * 16) {
+      auto from = [&](int k, int i) {
+        const int slot = i == 0 ? 2 * c0 + 1 : 2 * (c0 + i);
+        return a.part + ((size_t)slot * kRows + r0 + k) * a.pstride;
+      };
+      const int col = lane * 4;
+      float4 v[4][4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[k][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (r0 + k < rows && i < pieces && col < d)
+            v[k][i] = *reinterpret_cast<const float4*>(from(k, i) + col);
+        }
+      float2 ml = make_float2(-CUDART_INF_F, 0.f);
+      if (lane < 16 && r0 + (lane >> 2) < rows && (lane & 3) < pieces)
+        ml = *reinterpret_cast<const float2*>(from(lane >> 2, lane & 3) + a.pstride - 4);
+      float M = fmaxf(ml.x, __shfl_xor_sync(0xffffffffu, ml.x, 1));
+      M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 2));
+      const float wt = ml.x == -CUDART_INF_F ? 0.f : attn_ex2(ml.x - M);
+      float l = ml.x == -CUDART_INF_F ? ml.y : ml.y * wt;
+      l += __shfl_xor_sync(0xffffffffu, l, 1);
+      l += __shfl_xor_sync(0xffffffffu, l, 2);
+      if (lane < 16 && (lane & 3) == 0 && r0 + (lane >> 2) < rows)
+        attn_put_lse(a, attn_row(a, b, w.h, rt * kRows + r0 + (lane >> 2)), M, l);
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float f = __shfl_sync(0xffffffffu, wt, 4 * k + i);
+          o.x = fmaf(f, v[k][i].x, o.x);
+          o.y = fmaf(f, v[k][i].y, o.y);
+          o.z = fmaf(f, v[k][i].z, o.z);
+          o.w = fmaf(f, v[k][i].w, o.w);
+        }
+        const float f = __shfl_sync(0xffffffffu, inv, 4 * k);
+        if (r0 + k < rows && col < d) {
+          const AttnRow x = attn_row(a, b, w.h, rt * kRows + r0 + k);
+          __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) + x.b * a.os[0] +
+                               x.hq * a.os[1] + x.t * a.os[2];
+          *reinterpret_cast<uint2*>(out + col) =
+              make_uint2(pack_bf16(o.x * f, o.y * f), pack_bf16(o.z * f, o.w * f));
+        }
+      }
+    }
+    return;
+  }
   for (int r = blockIdx.y * 4 + warp; r < rows; r += gridDim.y * 4) {
     auto piece = [&](int i) {
       const int slot = i == 0 ? 2 * c0 + 1 : 2 * (c0 + i);
-      return a.part + ((size_t)slot * unit_rows + r) * a.pstride;
+      return a.part + ((size_t)slot * kRows + r) * a.pstride;
     };
-    float M = -CUDART_INF_F, ls = 0.f;
-    for (int i = lane; i < pieces; i += 32) {
-      const float2 ml = *reinterpret_cast<const float2*>(piece(i) + a.pstride - 4);
-      const float nm = fmaxf(M, ml.x);
-      if (nm != -CUDART_INF_F || !(ml.y == 0.f)) {
-        const float mu = nm == -CUDART_INF_F ? 0.f : nm;
-        ls = ls * attn_ex2(M - mu) + ml.y * attn_ex2(ml.x - mu);
-      }
-      M = nm;
-    }
-    const float Mall = warp_max(M);
-    const float mu = Mall == -CUDART_INF_F ? 0.f : Mall;
-    const float l = warp_sum(ls * attn_ex2(M - mu));
+    float4 v[kFly];
+#pragma unroll
+    for (int k = 0; k < kFly; ++k)
+      if (k < pieces && lane * 4 < d) v[k] = *reinterpret_cast<const float4*>(piece(k) + lane * 4);
+    auto stats = [&](int i) {
+      return i < pieces ? *reinterpret_cast<const float2*>(piece(i) + a.pstride - 4)
+                        : make_float2(-CUDART_INF_F, 0.f);
+    };
+    float2 ml = stats(lane);  // of piece i0 + lane
+    float M = ml.x;
+    for (int i0 = 32; i0 < pieces; i0 += 32) M = fmaxf(M, stats(i0 + lane).x);
+    M = warp_max(M);
+    auto weight = [&](float2 y) { return y.x == -CUDART_INF_F ? 0.f : attn_ex2(y.x - M); };
+    auto sum_of = [&](float2 y) { return y.x == -CUDART_INF_F ? y.y : y.y * weight(y); };
+    float l = sum_of(ml);
+    for (int i0 = 32; i0 < pieces; i0 += 32) l += sum_of(stats(i0 + lane));
+    l = warp_sum(l);
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    const AttnRow x = attn_row(a, b, de.y, rt * unit_rows + r);
+    const AttnRow x = attn_row(a, b, w.h, rt * kRows + r);
     TQ* out = reinterpret_cast<TQ*>(a.out) + x.b * a.os[0] + x.hq * a.os[1] + x.t * a.os[2];
-    for (int col = lane * 4; col < d; col += 128) {
+    for (int c = 0; c < d; c += 128) {
+      const int col = c + lane * 4;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int i0 = 0; i0 < pieces; i0 += 4) {
-        float4 v[4];
-        float wt[4];
+      for (int i0 = 0; i0 < pieces; i0 += 32) {
+        const float wt = weight(i0 == 0 ? ml : stats(i0 + lane));
+        const int end = min(32, pieces - i0);
+        for (int k0 = 0; k0 < end; k0 += kFly) {
+          if (i0 + k0 + c > 0) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (i0 + k >= pieces) break;
-          const float* p = piece(i0 + k);
-          v[k] = *reinterpret_cast<const float4*>(p + col);
-          wt[k] = p[a.pstride - 4];
-        }
+            for (int k = 0; k < kFly; ++k)
+              if (k0 + k < end && col < d)
+                v[k] = *reinterpret_cast<const float4*>(piece(i0 + k0 + k) + col);
+          }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (i0 + k >= pieces) break;
-          const float f = wt[k] == -CUDART_INF_F ? 0.f : attn_ex2(wt[k] - mu);
-          o.x = fmaf(f, v[k].x, o.x);
-          o.y = fmaf(f, v[k].y, o.y);
-          o.z = fmaf(f, v[k].z, o.z);
-          o.w = fmaf(f, v[k].w, o.w);
+          for (int k = 0; k < kFly; ++k) {
+            const float f = __shfl_sync(0xffffffffu, wt, (k0 + k) & 31);
+            if (k0 + k < end && col < d) {
+              o.x = fmaf(f, v[k].x, o.x);
+              o.y = fmaf(f, v[k].y, o.y);
+              o.z = fmaf(f, v[k].z, o.z);
+              o.w = fmaf(f, v[k].w, o.w);
+            }
+          }
         }
       }
       const float y[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
+      if (sizeof(TQ) == 2 && d % 4 == 0 && ((uintptr_t)out & 7) == 0) {
+        if (col < d)
+          *reinterpret_cast<uint2*>(out + col) =
+              make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+      } else {
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (col + k < d) store_out(out + col + k, y[k]);
+        for (int k = 0; k < 4; ++k)
+          if (col + k < d) store_out(out + col + k, y[k]);
+      }
     }
-    if (lane == 0) attn_put_lse(a, x, Mall, l);
+    if (lane == 0) attn_put_lse(a, x, M, l);
   }
 }
 
 template <typename TQ, typename TP>
 cudaError_t launch_simt(const AttnDev& a, cudaStream_t st) {
-  const size_t smem =
-      ((size_t)(kSRows + 2 * kSTile) * row_stride(a.c.d) + 4 * kSTile * 4) * sizeof(float);
+  auto bytes = [](int d) {
+    return ((size_t)(kSRows + 2 * kSTile) * row_stride(d) + 4 * kSTile * 4) * sizeof(float);
+  };
+  const size_t smem = bytes(a.c.d);
   const auto kern = k_attn_simt<TQ, TP>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = allow_smem<k_attn_simt<TQ, TP>>((int)bytes(256));
   if (e != cudaSuccess) return e;
   kern<<<kSCtas, kSThreads, smem, st>>>(a);
   return cudaGetLastError();
@@ -295,7 +415,7 @@ cudaError_t launch_simt(const AttnDev& a, cudaStream_t st) {
 
 }  // namespace
 
-AttnGrid attn_grid_simt() { return {kSCtas, kSRows}; }
+AttnGrid attn_grid_simt() { return {kSCtas, kSRows, kSTile}; }
 
 cudaError_t launch_attn_simt(const AttnDev& a, int page_dtype, int q_dtype, cudaStream_t st) {
   if (q_dtype == DROPKV_BF16) {
@@ -308,11 +428,23 @@ cudaError_t launch_attn_simt(const AttnDev& a, int page_dtype, int q_dtype, cuda
   return launch_simt<float, E4M3>(a, st);
 }
 
-cudaError_t launch_attn_merge(const AttnDev& a, int ctas, int rows, int q_dtype, cudaStream_t st) {
-  const dim3 grid((unsigned)ctas, (unsigned)((rows + 15) / 16));
-  if (q_dtype == DROPKV_BF16)
-    return launch_ex(k_attn_merge<__nv_bfloat16>, grid, dim3(128), 0, st, true, 1, a, rows);
-  return launch_ex(k_attn_merge<float>, grid, dim3(128), 0, st, true, 1, a, rows);
+template <typename TQ, int kRows, int kTile>
+cudaError_t launch_merge(const AttnDev& a, int ctas, cudaStream_t st) {
+  // a warp per row or two; per eight rows of the largest units, which are cut
+  // into few pieces
+  const int most = a.G * a.T < kRows ? a.G * a.T : kRows;
+  const int per = kRows == 256 ? 32 : kRows == 128 ? 8 : 4;
+  return launch_ex(k_attn_merge<TQ, kRows, kTile>, dim3(ctas, (most + per - 1) / per), dim3(128), 0,
+                   st, true, 1, a, ctas);
+}
+
+cudaError_t launch_attn_merge(const AttnDev& a, AttnGrid g, int q_dtype, cudaStream_t st) {
+  if (q_dtype == DROPKV_F32) return launch_merge<float, kSRows, kSTile>(a, g.ctas, st);
+  if (g.tile == kSTile) return launch_merge<__nv_bfloat16, kSRows, kSTile>(a, g.ctas, st);
+  if (g.rows == 8) return launch_merge<__nv_bfloat16, 8, 128>(a, g.ctas, st);
+  if (g.rows == 16) return launch_merge<__nv_bfloat16, 16, 128>(a, g.ctas, st);
+  if (g.rows == 128) return launch_merge<__nv_bfloat16, 128, 128>(a, g.ctas, st);
+  return launch_merge<__nv_bfloat16, 256, 128>(a, g.ctas, st);
 }
 
 }  // namespace dropkv

@@ -158,11 +158,6 @@ __device__ __forceinline__ uint32_t without_non_finite(uint32_t two) {
   return two;
 }
 
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
 // A row scale 2^(byte - 127) as two bf16 factors for the bits of e4m3 on their
 // way to bf16 (the seven magnitude bits at the bottom of the exponent: the value
 // times 2^-120): 2^(byte - 7), 2^127 at most, in the lower half; the rest, 1 but
@@ -171,16 +166,6 @@ __device__ __forceinline__ uint32_t widen_factors(uint32_t byte) {
   if (byte == 255u) return 0x3F807FC0u;
   return ((min(byte, 134u) + 120u) << 7) | (byte <= 134u ? 0x3F80u : (byte - 134u + 127u) << 7) << 16;
 }
-// Two e4m3 bytes of x to a bf16 pair, times f: the bytes, sign-extended to 16
-// bits each (kSel: byte i and its sign, byte j and its sign), four bits up, less
-// the copies of the sign between sign and exponent.
-template <uint32_t kSel>
-__device__ __forceinline__ uint32_t widen2(uint32_t x, uint32_t f) {
-  uint32_t z;
-  asm("prmt.b32 %0, %1, %1, %2;" : "=r"(z) : "r"(x), "n"(kSel));
-  return mul_bf16x2((z << 4) & 0x87F087F0u, f);
-}
-
 // 2^x of two values without the special-function unit: n = x rounded to an
 // integer by the addition of 1.5 2^23, 2^(x - n) on [-1/2, 1/2] by a polynomial of
 // degree 4 fitted for the least relative error (2.9e-6) under p(0) = 1, and n
@@ -284,10 +269,7 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
   pdl_trigger();
   const uint32_t base = smem_u32(sm);
   if (base & 1023u) {  // the swizzled tiles need 1 KB alignment
-    if (threadIdx.x == 0) {
-      a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
-      if (a.status) atomicMax(a.status, (int)DROPKV_ERR_CUDA);
-    }
+    if (threadIdx.x == 0 && a.status) atomicMax(a.status, (int)DROPKV_ERR_CUDA);
     return;
   }
   AttnPlanShared& plan = *reinterpret_cast<AttnPlanShared*>(sm + S::oPlan);
@@ -330,7 +312,6 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
       mbar_init(UE(u), 8);
       sodd[u] = 0;
     }
-    a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
     fence_mbar_init();
   }
   if (warp == kTMmaWarp) {
@@ -338,10 +319,8 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
     tmem_relinquish();
     tc_fence_before();
   }
-  int64_t total;
-  int grid;
   AttnWalk w;
-  bool more = attn_plan<kRows, kTTile, kTThreads>(a, plan, w, total, grid);
+  bool more = attn_plan<kRows, kTTile, kTThreads>(a, plan, w);
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
@@ -581,8 +560,8 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
           const uint32_t f2 = __byte_perm(f, 0, 0x1010);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            y[2 * k] = widen2<0x9180>(in[k], f2);
-            y[2 * k + 1] = widen2<0xB3A2>(in[k], f2);
+            y[2 * k] = widen_e4m3x2<kBytes01>(in[k], f2);
+            y[2 * k + 1] = widen_e4m3x2<kBytes23>(in[k], f2);
           }
         };
         auto store = [&](uint32_t src, uint32_t byte, uint32_t dst, int part) {
@@ -906,7 +885,6 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
         tc_fence_before();
         named_barrier_sync(1, 256);  // O and xml are read out
       }
-      if (slot >= 0 && (slot & 1) && threadIdx.x == 0) attn_describe(a, w, total, grid);
       __syncwarp();
       if (lane == 0) mbar_arrive(UE(units & 1));
       tiles += T;
@@ -927,7 +905,7 @@ cudaError_t launch_tile(const AttnDev& a, cudaStream_t st) {
   const auto kern = k_attn_tile<TP, D, kAlt>;
   constexpr int smem = TileShared<TP, D, kAlt>::kBytes;
   static_assert(smem <= 232448, "shared memory of a CTA");
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = allow_smem<k_attn_tile<TP, D, kAlt>>(smem);
   if (e != cudaSuccess) return e;
   kern<<<kTCtas, kTThreads, smem, st>>>(a);
   return cudaGetLastError();
@@ -943,7 +921,7 @@ cudaError_t launch_tiles(const AttnDev& a, int page_dtype, cudaStream_t st) {
 
 }  // namespace
 
-AttnGrid attn_grid_tile(bool alt) { return {kTCtas, alt ? 128 : 256}; }
+AttnGrid attn_grid_tile(bool alt) { return {kTCtas, alt ? 128 : 256, kTTile}; }
 
 cudaError_t launch_attn_tile(const AttnDev& a, int page_dtype, bool alt, cudaStream_t st) {
   return alt ? launch_tiles<true>(a, page_dtype, st) : launch_tiles<false>(a, page_dtype, st);
