@@ -109,7 +109,7 @@ __device__ __forceinline__ void widen_rows(const AttnDev& a, float* sK, float* s
 }
 
 template <typename TQ, typename TP>
-__global__ void __launch_bounds__(kSThreads) k_attn_simt(const AttnDev a) {
+__global__ void __launch_bounds__(kSThreads, 4) k_attn_simt(const AttnDev a) {
   extern __shared__ __align__(16) float sm[];
   __shared__ AttnPlanShared plan;
   __shared__ int64_t srow[2][kSTile];  // pool rows of a tile's slots, -1: none
@@ -170,6 +170,7 @@ __global__ void __launch_bounds__(kSThreads) k_attn_simt(const AttnDev a) {
       if (warp * 4 < rows) {
         const int slot = t * kSTile + lane;
         float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
         for (int i = 0; i < d; i += 4) {
           const float4 k4 = four(sK + lane * ds + i);
 #pragma unroll
@@ -200,22 +201,40 @@ __global__ void __launch_bounds__(kSThreads) k_attn_simt(const AttnDev a) {
         partly = __any_sync(0xffffffffu, partly);
         *reinterpret_cast<float4*>(sP + lane * 4) = make_float4(p[0], p[1], p[2], p[3]);
         __syncwarp();
-        for (int j = 0; j < kSTile; ++j) {
-          const float4 p4 = four(sP + j * 4);
-          const float* v = sV + j * ds;
-          const int sj = t * kSTile + j;
-          // a slot that a row does not see may hold anything: 0 * NaN must not
-          // reach that row
-          const bool u0 = !partly || sj < seen[0], u1 = !partly || sj < seen[1];
-          const bool u2 = !partly || sj < seen[2], u3 = !partly || sj < seen[3];
+        if (!partly) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            if (lane + 32 * i >= d) break;
-            const float x = v[lane + 32 * i];
-            if (u0) o[0][i] = fmaf(p4.x, x, o[0][i]);
-            if (u1) o[1][i] = fmaf(p4.y, x, o[1][i]);
-            if (u2) o[2][i] = fmaf(p4.z, x, o[2][i]);
-            if (u3) o[3][i] = fmaf(p4.w, x, o[3][i]);
+            const int col = lane + 32 * i;
+            if (32 * i >= d) break;
+            const float* v = sV + (col < d ? col : 0);
+#pragma unroll 8
+            for (int j = 0; j < kSTile; ++j) {
+              const float4 p4 = four(sP + j * 4);
+              const float x = v[j * ds];
+              o[0][i] = fmaf(p4.x, x, o[0][i]);
+              o[1][i] = fmaf(p4.y, x, o[1][i]);
+              o[2][i] = fmaf(p4.z, x, o[2][i]);
+              o[3][i] = fmaf(p4.w, x, o[3][i]);
+            }
+          }
+        } else {
+          // a slot that a row does not see may hold anything: 0 * NaN must not
+          // reach that row
+#pragma unroll 1
+          for (int j = 0; j < kSTile; ++j) {
+            const float4 p4 = four(sP + j * 4);
+            const float* v = sV + j * ds;
+            const int sj = t * kSTile + j;
+            const bool u0 = sj < seen[0], u1 = sj < seen[1], u2 = sj < seen[2], u3 = sj < seen[3];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              if (lane + 32 * i >= d) break;
+              const float x = v[lane + 32 * i];
+              if (u0) o[0][i] = fmaf(p4.x, x, o[0][i]);
+              if (u1) o[1][i] = fmaf(p4.y, x, o[1][i]);
+              if (u2) o[2][i] = fmaf(p4.z, x, o[2][i]);
+              if (u3) o[3][i] = fmaf(p4.w, x, o[3][i]);
+            }
           }
         }
       }
