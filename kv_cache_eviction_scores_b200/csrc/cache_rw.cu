@@ -146,24 +146,39 @@ __device__ __forceinline__ uint32_t to_scaled(float (&x)[8], int lanes) {
   return byte;
 }
 
+// The same for bf16 values of K and V on their way to e4m3, packed throughout: the
+// kernel issues instructions most of its time, and this takes two thirds of them.
+// |x| of bf16 orders like its bits, so one chain of shuffles finds both rows'
+// maxima as 16-bit halves.  The product with a power of two is exact in bf16, too,
+// where it matters: what falls below its range is far under e4m3's smallest step.
+__device__ __forceinline__ uint32_t abs_max(const uint4& w) {
+  constexpr uint32_t kAbs = 0x7FFF7FFFu;
+  const uint32_t m = __vmaxu2(__vmaxu2(w.x & kAbs, w.y & kAbs), __vmaxu2(w.z & kAbs, w.w & kAbs));
+  return max(m & 0xFFFFu, m >> 16);
+}
+__device__ __forceinline__ uint2 scaled_e4m3(const uint4& w, uint32_t byte) {
+  const uint32_t f = (byte == 255u ? 0x7FC0u : (254u - byte) << 7) * 0x10001u;
+  const uint32_t y[4] = {mul_bf16x2(w.x, f), mul_bf16x2(w.y, f), mul_bf16x2(w.z, f), mul_bf16x2(w.w, f)};
+  uint32_t z[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    z[i] = pack_e4m3(__uint_as_float(y[i] << 16), __uint_as_float(y[i] & 0xFFFF0000u));
+  return make_uint2(__byte_perm(z[0], z[1], 0x5410), __byte_perm(z[2], z[3], 0x5410));
+}
+
 // What a group of lanes moves in one go: its dense row and its row of the pools.
 struct Move {
-  int64_t dense;  // row of the dense tensors, < 0: nothing
   int64_t held;   // row of the pools
+  int32_t dense;  // row of the dense tensors, < 0: nothing
 };
 
-// Item i of (b, h).  kWrite: dense row i or rows[i], slot start + i; else dense
-// row i, slot start + (i or rows[i]).
+// Item i of (b, h), whose list entry (i without a list) is `at`.  kWrite: dense row
+// at, slot start + i; else dense row i, slot start + at.
 template <bool kWrite>
 __device__ __forceinline__ Move find(const CacheDev& c, const RowsDev& r, int b, int h, int i,
-                                     int cnt, int base) {
+                                     int at, int cnt, int base) {
   Move mv = {-1, -1};
-  if (i >= cnt) return mv;
-  int at = i;
-  if (r.rows) {
-    at = __ldg(r.rows + ((size_t)b * c.Hkv + h) * r.m + i);
-    if (at == -1) return mv;
-  }
+  if (i >= cnt || (r.rows && at == -1)) return mv;
   const int64_t slot = (int64_t)base + (kWrite ? i : at);
   const int dense = kWrite ? at : i;
   bool bad = at < 0 || dense >= r.n || slot < 0 || slot >= c.cap;
@@ -195,6 +210,12 @@ __global__ void __launch_bounds__(kThreads) k_cache_rows(const CacheDev c, const
   const int lane = threadIdx.x & (r.lanes - 1);
   const int per = kThreads / r.lanes;
   const int grp = threadIdx.x / r.lanes;
+  // the first list entry is requested together with the count and the start
+  const int first = blk * per * kRowsInFlight;
+  auto entry = [&](int i) {
+    return r.rows && i < r.m ? __ldg(r.rows + ((size_t)b * c.Hkv + h) * r.m + i) : i;
+  };
+  int at = entry(first + (int)threadIdx.x);
   int cnt = r.counts ? __ldg(r.counts + b) : r.m;
   if (cnt < 0 || cnt > r.m) {
     if (threadIdx.x == 0) raise_arg(r.status);
@@ -202,17 +223,23 @@ __global__ void __launch_bounds__(kThreads) k_cache_rows(const CacheDev c, const
   }
   const int base = r.start ? __ldg(r.start + b) : 0;
   constexpr bool kScaled = sizeof(TP) == 1;
-  const int i0 = blk * per * kRowsInFlight + grp;
-  if (blk * per * kRowsInFlight >= cnt) return;  // the whole block
+  if (first >= cnt) return;  // the whole block
 
   TD* const dk = reinterpret_cast<TD*>(r.k) + b * r.ks[0] + h * r.ks[1];
   TD* const dv = reinterpret_cast<TD*>(r.v) + b * r.vs[0] + h * r.vs[1];
   TP* const pk = reinterpret_cast<TP*>(c.k);
   TP* const pv = reinterpret_cast<TP*>(c.v);
+  // each of the block's rows is placed by one thread; done by every lane that
+  // moves a row, this was half of all instructions
+  __shared__ Move place[kThreads * kRowsInFlight];
+  for (int i = threadIdx.x; i < per * kRowsInFlight; i += kThreads) {
+    if (i >= kThreads) at = entry(first + i);
+    place[i] = find<kWrite>(c, r, b, h, first + i, at, cnt, base);
+  }
+  __syncthreads();
   Move mv[kRowsInFlight];
 #pragma unroll
-  for (int u = 0; u < kRowsInFlight; ++u)
-    mv[u] = find<kWrite>(c, r, b, h, i0 + u * per, cnt, base);
+  for (int u = 0; u < kRowsInFlight; ++u) mv[u] = place[u * per + grp];
   using From = typename Pick<kWrite, TD, TP>::type;
   Piece<kVec, From> xk[kRowsInFlight], xv[kRowsInFlight];
   uint32_t bk[kRowsInFlight], bv[kRowsInFlight];
@@ -234,34 +261,58 @@ __global__ void __launch_bounds__(kThreads) k_cache_rows(const CacheDev c, const
       }
     }
   }
+  if constexpr (kWrite && kVec && kScaled && sizeof(TD) == 2) {
+    uint32_t top[kRowsInFlight];
 #pragma unroll
-  for (int u = 0; u < kRowsInFlight; ++u) {
-    float yk[8], yv[8];
-    xk[u].get(yk);
-    xv[u].get(yv);
-    if (kWrite && kScaled) {  // every lane of the warp
-      bk[u] = to_scaled(yk, r.lanes);
-      bv[u] = to_scaled(yv, r.lanes);
+    for (int u = 0; u < kRowsInFlight; ++u) top[u] = abs_max(xk[u].s.w) | abs_max(xv[u].s.w) << 16;
+    for (int o = r.lanes >> 1; o > 0; o >>= 1)
+#pragma unroll
+      for (int u = 0; u < kRowsInFlight; ++u)
+        top[u] = __vmaxu2(top[u], __shfl_xor_sync(0xffffffffu, top[u], o));
+#pragma unroll
+    for (int u = 0; u < kRowsInFlight; ++u) {
+      if (mv[u].dense < 0) continue;
+      const uint32_t bk = scale_byte(top[u] << 16), bv = scale_byte(top[u] & 0xFFFF0000u);
+      if (lane * 8 < c.d) {
+        const int64_t at = mv[u].held * c.d + lane * 8;
+        *reinterpret_cast<uint2*>(pk + at) = scaled_e4m3(xk[u].s.w, bk);
+        *reinterpret_cast<uint2*>(pv + at) = scaled_e4m3(xv[u].s.w, bv);
+      }
+      if (lane == 0) {
+        c.ks[mv[u].held] = (uint8_t)bk;
+        c.vs[mv[u].held] = (uint8_t)bv;
+      }
     }
-    if (mv[u].dense < 0) continue;
-    if constexpr (kWrite) {
-      store8<kVec>(pk + mv[u].held * c.d, lane, c.d, yk);
-      store8<kVec>(pv + mv[u].held * c.d, lane, c.d, yv);
-      if (kScaled && lane == 0) {
-        c.ks[mv[u].held] = (uint8_t)bk[u];
-        c.vs[mv[u].held] = (uint8_t)bv[u];
-      }
-    } else {
-      if (kScaled) {
-        const float fk = scale_of(bk[u]), fv = scale_of(bv[u]);
+  } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          yk[j] *= fk;
-          yv[j] *= fv;
-        }
+    for (int u = 0; u < kRowsInFlight; ++u) {
+      float yk[8], yv[8];
+      xk[u].get(yk);
+      xv[u].get(yv);
+      if (kWrite && kScaled) {  // every lane of the warp
+        bk[u] = to_scaled(yk, r.lanes);
+        bv[u] = to_scaled(yv, r.lanes);
       }
-      store8<kVec>(dk + mv[u].dense * r.ks[2], lane, c.d, yk);
-      store8<kVec>(dv + mv[u].dense * r.vs[2], lane, c.d, yv);
+      if (mv[u].dense < 0) continue;
+      if constexpr (kWrite) {
+        store8<kVec>(pk + mv[u].held * c.d, lane, c.d, yk);
+        store8<kVec>(pv + mv[u].held * c.d, lane, c.d, yv);
+        if (kScaled && lane == 0) {
+          c.ks[mv[u].held] = (uint8_t)bk[u];
+          c.vs[mv[u].held] = (uint8_t)bv[u];
+        }
+      } else {
+        if (kScaled) {
+          const float fk = scale_of(bk[u]), fv = scale_of(bv[u]);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            yk[j] *= fk;
+            yv[j] *= fv;
+          }
+        }
+        store8<kVec>(dk + mv[u].dense * r.ks[2], lane, c.d, yk);
+        store8<kVec>(dv + mv[u].dense * r.vs[2], lane, c.d, yv);
+      }
     }
   }
 }
