@@ -54,11 +54,16 @@ int path_of(const dropkv_cache& c, const dropkv_cache_attn& t) {
   return t.path == DROPKV_PATH_TENSOR ? -1 : DROPKV_PATH_SIMT;
 }
 
+// Query rows a KV head can have.
+int64_t group_rows(const dropkv_cache& c, const dropkv_cache_attn& t) {
+  return (int64_t)(t.Hq / c.Hkv) * t.T;
+}
+
 // The tensor path's kernel by the rows a KV head can have: eight as columns, or
 // 16 as rows, of warp-level products; or query tiles of 128 rows.
 enum class Tensor { kFew, kRows, kTile128, kTile256 };
 Tensor tensor_of(const dropkv_cache& c, const dropkv_cache_attn& t) {
-  const int64_t rows = (int64_t)(t.Hq / c.Hkv) * t.T;
+  const int64_t rows = group_rows(c, t);
   return rows <= 8     ? Tensor::kFew
          : rows <= 16  ? Tensor::kRows
          : rows <= 128 ? Tensor::kTile128
@@ -84,7 +89,7 @@ extern "C" size_t dropkv_cache_attention_workspace_bytes(const dropkv_cache* cac
                                                          const dropkv_cache_attn* attn) {
   if (check_attn(cache, attn, false) != DROPKV_OK) return 0;
   // the alignment of q and out is not known here: enough for either path
-  const size_t simt = layout(*cache, attn_grid_simt());
+  const size_t simt = layout(*cache, attn_grid_simt(group_rows(*cache, *attn), cache->d));
   if (attn->path == DROPKV_PATH_SIMT || !tensor_sizes(*cache, *attn)) return simt;
   const size_t tensor = layout(*cache, grid_of(tensor_of(*cache, *attn), cache->dtype));
   return std::max(simt, tensor);
@@ -119,7 +124,7 @@ extern "C" dropkv_status dropkv_cache_attention(const dropkv_cache* cache,
 
   const bool tensor = path == DROPKV_PATH_TENSOR;
   const Tensor kind = tensor_of(c, t);
-  const AttnGrid g = tensor ? grid_of(kind, c.dtype) : attn_grid_simt();
+  const AttnGrid g = tensor ? grid_of(kind, c.dtype) : attn_grid_simt(group_rows(c, t), c.d);
   AttnDev a = {};
   a.c = cache_dev(c);
   a.q = t.q;
@@ -144,7 +149,7 @@ extern "C" dropkv_status dropkv_cache_attention(const dropkv_cache* cache,
   a.status = status_dev;
   cudaError_t e;
   if (!tensor)
-    e = launch_attn_simt(a, c.dtype, t.dtype, st);
+    e = launch_attn_simt(a, g, c.dtype, t.dtype, st);
   else if (kind == Tensor::kFew)
     e = launch_attn_few(a, c.dtype, st);
   else if (kind == Tensor::kRows)

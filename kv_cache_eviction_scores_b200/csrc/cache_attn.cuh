@@ -235,11 +235,12 @@ struct AttnGrid {
   int ctas, rows, tile;  // of a unit
 };
 // Grid and unit rows of each kernel (host); launchers of one call's kernels.
-AttnGrid attn_grid_simt();
+AttnGrid attn_grid_simt(int64_t rows, int d);  // rows a KV head can have
 AttnGrid attn_grid_rows();
 AttnGrid attn_grid_few(int page_dtype);
 AttnGrid attn_grid_tile(bool alt);
-cudaError_t launch_attn_simt(const AttnDev& a, int page_dtype, int q_dtype, cudaStream_t st);
+cudaError_t launch_attn_simt(const AttnDev& a, AttnGrid g, int page_dtype, int q_dtype,
+                             cudaStream_t st);
 cudaError_t launch_attn_rows(const AttnDev& a, int page_dtype, cudaStream_t st);
 cudaError_t launch_attn_few(const AttnDev& a, int page_dtype, cudaStream_t st);
 cudaError_t launch_attn_tile(const AttnDev& a, int page_dtype, bool alt, cudaStream_t st);

@@ -10,12 +10,15 @@
 // each 32.  The rows' stride is an odd number of 16-byte pieces, so that the
 // lanes' float4 reads of 32 rows touch every bank evenly.
 #include "cache_attn.cuh"
+#include "tc_ptx.cuh"
 
 namespace dropkv {
 
 namespace {
 
-constexpr int kSRows = 16, kSTile = 32, kSThreads = 128, kSCtas = 592;  // four CTAs an SM
+constexpr int kSRows = 16, kSTile = 32, kSThreads = 128;
+constexpr int kSCtas = 592;                  // four CTAs an SM
+constexpr int kLCtas = 296, kLCtas3 = 444;   // of the 64-row kernel two, for d <= 64 three
 
 __device__ __forceinline__ float4 four(const float* p) { return *reinterpret_cast<const float4*>(p); }
 __device__ __forceinline__ float single(const float* p) { return *p; }
@@ -188,11 +191,12 @@ __global__ void __launch_bounds__(kSThreads, 4) k_attn_simt(const AttnDev a) {
         for (int k = 0; k < 4; ++k) {
           const bool hid = slot >= seen[k] || absent;
           partly = partly || (live[k] && hid);
-          const float y = hid ? -CUDART_INF_F : s[k] * a.c_log2;
-          const float mt = fmaxf(m[k], warp_max(y));
+          // c > 0 commutes with the max; the one rounding of s c - mu is relative to
+          // that difference, and mu's own is the same for the whole row
+          const float mt = fmaxf(m[k], warp_max(hid ? -CUDART_INF_F : s[k]) * a.c_log2);
           const float mu = mt == -CUDART_INF_F ? 0.f : mt;
           const float fac = attn_ex2(m[k] - mu);
-          p[k] = hid ? 0.f : attn_ex2(y - mu);
+          p[k] = hid ? 0.f : attn_ex2(fmaf(s[k], a.c_log2, -mu));
           m[k] = mt;
           l[k] = l[k] * fac + warp_sum(p[k]);
 #pragma unroll
@@ -265,6 +269,232 @@ __global__ void __launch_bounds__(kSThreads, 4) k_attn_simt(const AttnDev a) {
   }
 }
 
+// ---- many rows per KV head -----------------------------------------------------
+//
+// k_attn_simt_tile: a unit is 64 query rows against tiles of 32 slots, 128 threads.
+// Thread (ty, tx) computes the logits of rows 4 ty .. 4 ty + 3 and slots tx + 8 j (j
+// < 4) from float4 pieces, eight 16-byte loads for 64 multiply-adds (32 packed
+// ones), keeps those rows' statistics with its seven neighbours, and owns columns 4
+// tx .. 4 tx + 3 of every 32 of those rows' O.  The rows' stride, an odd number of
+// 16-byte pieces, keeps the eight slots' loads in different banks.
+constexpr int kLRows = 64, kPStride = kSTile + 4;
+
+__device__ __forceinline__ uint64_t lo2(const float4& v) { return tc::pk2(v.x, v.y); }
+__device__ __forceinline__ uint64_t hi2(const float4& v) { return tc::pk2(v.z, v.w); }
+
+template <typename TQ, typename TP, int kCols>  // kCols: blocks of 32 columns
+__global__ void __launch_bounds__(kSThreads, kCols > 4 ? 1 : kCols > 2 ? 2 : 3) k_attn_simt_tile(const AttnDev a) {
+  extern __shared__ __align__(16) float sm[];
+  __shared__ AttnPlanShared plan;
+  __shared__ int64_t srow[2][kSTile];  // pool rows of a tile's slots, -1: none
+  pdl_trigger();
+  const int d = a.c.d, ds = row_stride(d), d4 = (d + 3) & ~3;
+  float* sQ = sm;
+  float* sK = sQ + kLRows * ds;
+  float* sV = sK + kSTile * ds;
+  float* sP = sV + kSTile * ds;  // [kLRows][kPStride]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int ty = threadIdx.x >> 3, tx = threadIdx.x & 7;
+  AttnWalk w;
+  bool more = attn_plan<kLRows, kSTile, kSThreads>(a, plan, w);
+  while (more) {
+    const int b = w.item / a.nrt, rt = w.item - b * a.nrt;
+    int L, n;
+    attn_lengths(a, b, L, n);
+    const int rows = min(kLRows, a.G * n - rt * kLRows);
+    const int seen_all = attn_seen(a, L, n, rt * kLRows + rows - 1);
+    const int seen_min = attn_seen(a, L, n, rt * kLRows);
+    __syncthreads();  // the last unit's reads of shared memory
+#pragma unroll 4
+    for (int r = warp; r < kLRows; r += 4) {
+      const AttnRow x = attn_row(a, b, w.h, rt * kLRows + (r < rows ? r : 0));
+      const TQ* q = reinterpret_cast<const TQ*>(a.q) + x.b * a.qs[0] + x.hq * a.qs[1] + x.t * a.qs[2];
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) {
+        const int col = lane + 32 * i;
+        if (col < d4) sQ[r * ds + col] = r < rows && col < d ? single(q + col) : 0.f;
+      }
+    }
+    auto place = [&](int t) {  // warp 0: the pool rows of tile t
+      const int slot = t * kSTile + lane;
+      int64_t row = -1;
+      if (slot < seen_all) {
+        row = cache_row(a.c, b, w.h, slot);
+        if (row < 0) raise_arg(a.status);
+      }
+      srow[t & 1][lane] = row;
+    };
+    if (warp == 0) place(w.t0);
+    int seen[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      seen[k] = 4 * ty + k < rows ? attn_seen(a, L, n, rt * kLRows + 4 * ty + k) : 0;
+    float m[4], l[4];
+    uint64_t o[4][kCols][2];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      m[k] = -CUDART_INF_F;
+      l[k] = 0.f;
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) o[k][i][0] = o[k][i][1] = 0ull;
+    }
+    __syncthreads();
+    for (int t = w.t0; t < w.t1; ++t) {
+      widen_rows<TP>(a, sK, sV, ds, srow[t & 1], warp, lane);
+      // the slots of the tile that are there
+      const uint32_t there = __ballot_sync(0xffffffffu, srow[t & 1][lane] >= 0);
+      if (warp == 0 && t + 1 < w.t1) place(t + 1);
+      __syncthreads();
+      if (4 * 4 * warp < rows) {
+        uint64_t acc[4][4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[k][j] = 0ull;
+#pragma unroll 2
+        for (int i = 0; i < d; i += 4) {
+          uint64_t ka[4], kb[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float4 k4 = four(sK + (tx + 8 * j) * ds + i);
+            ka[j] = lo2(k4);
+            kb[j] = hi2(k4);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float4 q4 = four(sQ + (4 * ty + k) * ds + i);
+            const uint64_t qa = lo2(q4), qb = hi2(q4);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[k][j] = tc::ffma2(qb, kb[j], tc::ffma2(qa, ka[j], acc[k][j]));
+          }
+        }
+        // some row of the unit does not see some slot of the tile
+        const bool partly = there != 0xFFFFFFFFu || (t + 1) * kSTile > seen_min;
+        const int lim = t * kSTile;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float s[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float x, y;
+            tc::upk2(acc[k][j], x, y);
+            s[j] = x + y;
+          }
+          bool hid[4] = {false, false, false, false};
+          float top = -CUDART_INF_F;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (partly) hid[j] = lim + tx + 8 * j >= seen[k] || !((there >> (tx + 8 * j)) & 1);
+            if (!hid[j]) top = fmaxf(top, s[j]);
+          }
+#pragma unroll
+          for (int x = 1; x < 8; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+          // as in the kernel above: one rounding, relative to the difference
+          const float mt = fmaxf(m[k], top * a.c_log2);
+          const float mu = mt == -CUDART_INF_F ? 0.f : mt;
+          if (mt != m[k]) {  // the same for the eight threads of the row
+            const float fac = attn_ex2(m[k] - mu);
+            m[k] = mt;
+            l[k] *= fac;
+            const uint64_t f2 = tc::pk2(fac, fac);
+#pragma unroll
+            for (int i = 0; i < kCols; ++i) {
+              o[k][i][0] = tc::fmul2(o[k][i][0], f2);
+              o[k][i][1] = tc::fmul2(o[k][i][1], f2);
+            }
+          }
+          float sum = 0.f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float p = hid[j] ? 0.f : attn_ex2(fmaf(s[j], a.c_log2, -mu));
+            sum += p;
+            sP[(4 * ty + k) * kPStride + tx + 8 * j] = p;
+          }
+          l[k] += sum;
+        }
+        __syncwarp();
+        if (!partly) {
+#pragma unroll 1
+          for (int j = 0; j < kSTile; j += 4) {
+            float4 p[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) p[k] = four(sP + (4 * ty + k) * kPStride + j);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float* v = sV + (j + e) * ds;
+#pragma unroll
+              for (int i = 0; i < kCols; ++i) {
+                const float4 x = four(v + min(4 * tx + 32 * i, d4 - 4));
+                const uint64_t xa = lo2(x), xb = hi2(x);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const float pe = e == 0 ? p[k].x : e == 1 ? p[k].y : e == 2 ? p[k].z : p[k].w;
+                  const uint64_t p2 = tc::pk2(pe, pe);
+                  o[k][i][0] = tc::ffma2(p2, xa, o[k][i][0]);
+                  o[k][i][1] = tc::ffma2(p2, xb, o[k][i][1]);
+                }
+              }
+            }
+          }
+        } else {
+          // a slot that a row does not see may hold anything: 0 * NaN must not
+          // reach that row
+#pragma unroll 1
+          for (int j = 0; j < kSTile; ++j) {
+            const float* v = sV + j * ds;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (lim + j >= seen[k] || !((there >> j) & 1)) continue;
+              const float pe = sP[(4 * ty + k) * kPStride + j];
+              const uint64_t p2 = tc::pk2(pe, pe);
+#pragma unroll
+              for (int i = 0; i < kCols; ++i) {
+                const float4 x = four(v + min(4 * tx + 32 * i, d4 - 4));
+                o[k][i][0] = tc::ffma2(p2, lo2(x), o[k][i][0]);
+                o[k][i][1] = tc::ffma2(p2, hi2(x), o[k][i][1]);
+              }
+            }
+          }
+        }
+      }
+      __syncthreads();
+    }
+    const int slot = attn_slot(w);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+#pragma unroll
+      for (int x = 1; x < 8; x <<= 1) l[k] += __shfl_xor_sync(0xffffffffu, l[k], x);
+      const int r = 4 * ty + k;
+      if (r >= rows) continue;
+      const AttnRow x = attn_row(a, b, w.h, rt * kLRows + r);
+      TQ* out = reinterpret_cast<TQ*>(a.out) + x.b * a.os[0] + x.hq * a.os[1] + x.t * a.os[2];
+      float* part = a.part + ((size_t)(slot < 0 ? 0 : slot) * kLRows + r) * a.pstride;
+      const float inv = l[k] == 0.f ? 0.f : 1.f / l[k];
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) {
+        const int col = 4 * tx + 32 * i;
+        float y[4];
+        tc::upk2(o[k][i][0], y[0], y[1]);
+        tc::upk2(o[k][i][1], y[2], y[3]);
+        if (slot >= 0) {
+          if (col < d) *reinterpret_cast<float4*>(part + col) = make_float4(y[0], y[1], y[2], y[3]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (col + e < d) store_out(out + col + e, y[e] * inv);
+        }
+      }
+      if (tx == 0) {
+        if (slot < 0)
+          attn_put_lse(a, x, m[k], l[k]);
+        else
+          *reinterpret_cast<float2*>(part + a.pstride - 4) = make_float2(m[k], l[k]);
+      }
+    }
+    more = attn_next<kLRows, kSTile>(a, w);
+  }
+}
+
 // Joins the partials of the cut unit that began in CTA blockIdx.x: a warp per
 // row, the pieces in the order of their slots:
 //   M = max m_i, l = sum l_i 2^(m_i - M), O = sum O_i 2^(m_i - M) / l.
@@ -301,7 +531,7 @@ __global__ void __launch_bounds__(128) k_attn_merge(const AttnDev a, int ctas) {
   const int rows = min(kRows, a.G * n - rt * kRows);
   const int d = a.c.d;
   pdl_wait();
-  if (kRows > 16 && pieces <= 4) {
+  if (kRows >= 128 && pieces <= 4) {
     // large units are cut into few pieces: four rows at a time, lane 4 k + i with
     // row k's (m, l) of piece i
     for (int r0 = (blockIdx.y * 4 + warp) * 4; r0 < rows; r0 += gridDim.y * 16) {
@@ -432,19 +662,51 @@ cudaError_t launch_simt(const AttnDev& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+template <typename TQ, typename TP, int kCols>
+cudaError_t launch_simt_cols(const AttnDev& a, int ctas, cudaStream_t st) {
+  auto bytes = [](int d) {
+    return ((size_t)(kLRows + 2 * kSTile) * row_stride(d) + kLRows * kPStride) * sizeof(float);
+  };
+  cudaError_t e = allow_smem<k_attn_simt_tile<TQ, TP, kCols>>((int)bytes(32 * kCols));
+  if (e != cudaSuccess) return e;
+  k_attn_simt_tile<TQ, TP, kCols><<<ctas, kSThreads, bytes(a.c.d), st>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename TQ, typename TP>
+cudaError_t launch_simt_tile(const AttnDev& a, int ctas, cudaStream_t st) {
+  if (a.c.d <= 32) return launch_simt_cols<TQ, TP, 1>(a, ctas, st);
+  if (a.c.d <= 64) return launch_simt_cols<TQ, TP, 2>(a, ctas, st);
+  if (a.c.d <= 128) return launch_simt_cols<TQ, TP, 4>(a, ctas, st);
+  return launch_simt_cols<TQ, TP, 8>(a, ctas, st);
+}
+
 }  // namespace
 
-AttnGrid attn_grid_simt() { return {kSCtas, kSRows, kSTile}; }
+// Tiles of 64 rows where they are filled twice; below that, pieces of 16, which
+// read K and V again but leave more CTAs at work.  Both measured (fp32, d = 64):
+// 111 rows of 8 heads' worth over 1501 slots 33 and 47 us, 70 x 8 heads over 4000
+// 68 and 73, 420 x 8 over 3000 184 and 117, 1200 x 2 over 1000 53 and 55.
+AttnGrid attn_grid_simt(int64_t rows, int d) {
+  if (rows <= 128) return {kSCtas, kSRows, kSTile};
+  return {d <= 64 ? kLCtas3 : kLCtas, kLRows, kSTile};
+}
 
-cudaError_t launch_attn_simt(const AttnDev& a, int page_dtype, int q_dtype, cudaStream_t st) {
+template <typename TQ, typename TP>
+static cudaError_t launch_simt_types(const AttnDev& a, AttnGrid g, cudaStream_t st) {
+  return g.rows == kSRows ? launch_simt<TQ, TP>(a, st) : launch_simt_tile<TQ, TP>(a, g.ctas, st);
+}
+
+cudaError_t launch_attn_simt(const AttnDev& a, AttnGrid g, int page_dtype, int q_dtype,
+                             cudaStream_t st) {
   if (q_dtype == DROPKV_BF16) {
-    if (page_dtype == DROPKV_BF16) return launch_simt<__nv_bfloat16, __nv_bfloat16>(a, st);
-    if (page_dtype == DROPKV_F32) return launch_simt<__nv_bfloat16, float>(a, st);
-    return launch_simt<__nv_bfloat16, E4M3>(a, st);
+    if (page_dtype == DROPKV_BF16) return launch_simt_types<__nv_bfloat16, __nv_bfloat16>(a, g, st);
+    if (page_dtype == DROPKV_F32) return launch_simt_types<__nv_bfloat16, float>(a, g, st);
+    return launch_simt_types<__nv_bfloat16, E4M3>(a, g, st);
   }
-  if (page_dtype == DROPKV_BF16) return launch_simt<float, __nv_bfloat16>(a, st);
-  if (page_dtype == DROPKV_F32) return launch_simt<float, float>(a, st);
-  return launch_simt<float, E4M3>(a, st);
+  if (page_dtype == DROPKV_BF16) return launch_simt_types<float, __nv_bfloat16>(a, g, st);
+  if (page_dtype == DROPKV_F32) return launch_simt_types<float, float>(a, g, st);
+  return launch_simt_types<float, E4M3>(a, g, st);
 }
 
 template <typename TQ, int kRows, int kTile>
@@ -452,12 +714,15 @@ cudaError_t launch_merge(const AttnDev& a, int ctas, cudaStream_t st) {
   // a warp per row or two; per eight rows of the largest units, which are cut
   // into few pieces
   const int most = a.G * a.T < kRows ? a.G * a.T : kRows;
-  const int per = kRows == 256 ? 32 : kRows == 128 ? 8 : 4;
+  const int per = kRows == 256 ? 32 : kRows > 16 ? 8 : 4;
   return launch_ex(k_attn_merge<TQ, kRows, kTile>, dim3(ctas, (most + per - 1) / per), dim3(128), 0,
                    st, true, 1, a, ctas);
 }
 
 cudaError_t launch_attn_merge(const AttnDev& a, AttnGrid g, int q_dtype, cudaStream_t st) {
+  if (g.tile == kSTile && g.rows == kLRows)
+    return q_dtype == DROPKV_F32 ? launch_merge<float, kLRows, kSTile>(a, g.ctas, st)
+                                 : launch_merge<__nv_bfloat16, kLRows, kSTile>(a, g.ctas, st);
   if (q_dtype == DROPKV_F32) return launch_merge<float, kSRows, kSTile>(a, g.ctas, st);
   if (g.tile == kSTile) return launch_merge<__nv_bfloat16, kSRows, kSTile>(a, g.ctas, st);
   if (g.rows == 8) return launch_merge<__nv_bfloat16, 8, 128>(a, g.ctas, st);
