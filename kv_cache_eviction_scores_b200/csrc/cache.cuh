@@ -113,6 +113,15 @@ __device__ __forceinline__ uint32_t widen_e4m3x2(uint32_t x, uint32_t f) {
   return mul_bf16x2((z << 4) & 0x87F087F0u, f);
 }
 
+__device__ __forceinline__ bool non_finite(uint32_t two) {  // of a bf16 pair
+  return (two & 0x7F80u) == 0x7F80u || (two & 0x7F800000u) == 0x7F800000u;
+}
+__device__ __forceinline__ uint32_t without_non_finite(uint32_t two) {
+  if ((two & 0x7F80u) == 0x7F80u) two &= 0xFFFF0000u;
+  if ((two & 0x7F800000u) == 0x7F800000u) two &= 0x0000FFFFu;
+  return two;
+}
+
 CacheDev cache_dev(const dropkv_cache& c);
 
 // Allows `kern` `bytes` of dynamic shared memory, once per device (the bit of a

@@ -372,75 +372,80 @@ __global__ void __launch_bounds__(kRThreads, 1) k_attn_rows(const AttnDev a) {
         }
         const uint32_t pa[4] = {pack_bf16(p[0][0], p[0][1]), pack_bf16(p[0][2], p[0][3]),
                                 pack_bf16(p[1][0], p[1][1]), pack_bf16(p[1][2], p[1][3])};
-        bool odd = false;  // a hidden slot's V may be an infinity or a NaN
         if (!kScaled && partly) {
+          // A hidden slot's V may be an infinity or a NaN, and 0 * NaN must not
+          // reach the rows that do not see it: such values are added to the rows
+          // that do, and the products go without them.
+          bool odd = false;
           const int c = lane % kPieces;
+          auto piece = [&](int i) {
+            return reinterpret_cast<uint4*>(ring + st * 2 * S::kHalf + S::kHalf +
+                                            swz<kPieces>(lane / kPieces + i * kPerPass, c));
+          };
 #pragma unroll
           for (int i = 0; i < 16 / kPerPass; ++i) {
-            const uint4 v = *reinterpret_cast<const uint4*>(
-                ring + st * 2 * S::kHalf + S::kHalf + swz<kPieces>(lane / kPieces + i * kPerPass, c));
-            const uint32_t y[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              odd = odd || (y[k] & 0x7F80u) == 0x7F80u || (y[k] & 0x7F800000u) == 0x7F800000u;
+            const uint4 v = *piece(i);
+            odd = odd || non_finite(v.x) || non_finite(v.y) || non_finite(v.z) || non_finite(v.w);
           }
-          odd = __any_sync(0xffffffffu, odd);
-        }
-        if (!odd) {
-          if constexpr (kScaled) {
+          if (__any_sync(0xffffffffu, odd)) {
+#pragma unroll 1
+            for (int j = 0; j < 16; ++j) {
+              const int from = (lane & ~3) | ((j & 7) >> 1);
+              float w0 = 0.f, w1 = 0.f;
+              uint32_t h0 = 0;
 #pragma unroll
-            for (int c = 0; c < D / 16; c += 2) {
-              uint32_t r[4];  // slots 0-7 and 8-15 of piece c, then of piece c + 1
-              ldsm4t(r, tv + swz<kPieces>((mi & 1) * 8 + mr, c + (mi >> 1)));
+              for (int x = 0; x < 2; ++x)
 #pragma unroll
-              for (int u = 0; u < 2; ++u) {  // even dims of the piece, then the odd ones
-                mma16816(o[2 * (c + u)], pa, widen2<kBytes02>(r[2 * u]), widen2<kBytes02>(r[2 * u + 1]));
-                mma16816(o[2 * (c + u) + 1], pa, widen2<kBytes13>(r[2 * u]), widen2<kBytes13>(r[2 * u + 1]));
+                for (int e = 0; e < 2; ++e)
+                  if (x == (j >> 3) && e == (j & 1)) {
+                    w0 = p[x][e];
+                    w1 = p[x][2 + e];
+                    h0 = ((hid >> (4 * x + e)) & 1) | ((hid >> (4 * x + 2 + e)) & 1) << 1;
+                  }
+              w0 = __shfl_sync(0xffffffffu, w0, from);
+              w1 = __shfl_sync(0xffffffffu, w1, from);
+              h0 = __shfl_sync(0xffffffffu, h0, from);
+#pragma unroll
+              for (int cc = 0; cc < D / 8; ++cc) {
+                const uint32_t v2 = *reinterpret_cast<const uint32_t*>(
+                    ring + st * 2 * S::kHalf + S::kHalf + swz<kPieces>(j, cc % kPieces) + 4 * tq);
+                const uint32_t x2[2] = {v2 << 16, v2 & 0xFFFF0000u};
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  if ((x2[e] & 0x7F800000u) == 0x7F800000u) {
+                    if (!(h0 & 1)) o[cc][e] = fmaf(w0, __uint_as_float(x2[e]), o[cc][e]);
+                    if (!(h0 & 2)) o[cc][2 + e] = fmaf(w1, __uint_as_float(x2[e]), o[cc][2 + e]);
+                  }
               }
             }
-          } else {
+            __syncwarp();
 #pragma unroll
-            for (int c = 0; c < D / 8; c += 2) {
-              uint32_t r[4];
-              ldsm4t(r, tv + swz<kPieces>((mi & 1) * 8 + mr, c + (mi >> 1)));
-              mma16816(o[c], pa, r[0], r[1]);
-              mma16816(o[c + 1], pa, r[2], r[3]);
+            for (int i = 0; i < 16 / kPerPass; ++i) {
+              const uint4 v = *piece(i);
+              *piece(i) = make_uint4(without_non_finite(v.x), without_non_finite(v.y),
+                                     without_non_finite(v.z), without_non_finite(v.w));
+            }
+            __syncwarp();
+          }
+        }
+        if constexpr (kScaled) {
+#pragma unroll
+          for (int c = 0; c < D / 16; c += 2) {
+            uint32_t r[4];  // slots 0-7 and 8-15 of piece c, then of piece c + 1
+            ldsm4t(r, tv + swz<kPieces>((mi & 1) * 8 + mr, c + (mi >> 1)));
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {  // even dims of the piece, then the odd ones
+              mma16816(o[2 * (c + u)], pa, widen2<kBytes02>(r[2 * u]), widen2<kBytes02>(r[2 * u + 1]));
+              mma16816(o[2 * (c + u) + 1], pa, widen2<kBytes13>(r[2 * u]), widen2<kBytes13>(r[2 * u + 1]));
             }
           }
         } else {
-          // out of the ordinary: 0 * NaN must not reach the rows that do not
-          // see the slot, so P V by scalars over the slots that a row sees
-#pragma unroll 1
-          for (int j = 0; j < 16; ++j) {
-            const int from = (lane & ~3) | ((j & 7) >> 1);
-            float w0 = 0.f, w1 = 0.f;
-            uint32_t h0 = 0;
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                if (x == (j >> 3) && e == (j & 1)) {
-                  w0 = p[x][e];
-                  w1 = p[x][2 + e];
-                  h0 = ((hid >> (4 * x + e)) & 1) | ((hid >> (4 * x + 2 + e)) & 1) << 1;
-                }
-            w0 = __shfl_sync(0xffffffffu, w0, from);
-            w1 = __shfl_sync(0xffffffffu, w1, from);
-            h0 = __shfl_sync(0xffffffffu, h0, from);
-#pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
-              const uint32_t v2 = *reinterpret_cast<const uint32_t*>(
-                  ring + st * 2 * S::kHalf + S::kHalf + swz<kPieces>(j, c % kPieces) + 4 * tq);
-              const float va = __uint_as_float(v2 << 16), vb = __uint_as_float(v2 & 0xFFFF0000u);
-              if (!(h0 & 1)) {
-                o[c][0] = fmaf(w0, va, o[c][0]);
-                o[c][1] = fmaf(w0, vb, o[c][1]);
-              }
-              if (!(h0 & 2)) {
-                o[c][2] = fmaf(w1, va, o[c][2]);
-                o[c][3] = fmaf(w1, vb, o[c][3]);
-              }
-            }
+          for (int c = 0; c < D / 8; c += 2) {
+            uint32_t r[4];
+            ldsm4t(r, tv + swz<kPieces>((mi & 1) * 8 + mr, c + (mi >> 1)));
+            mma16816(o[c], pa, r[0], r[1]);
+            mma16816(o[c + 1], pa, r[2], r[3]);
           }
         }
       }
@@ -745,60 +750,69 @@ __global__ void __launch_bounds__(kRThreads, few_ctas_per_sm<TP>()) k_attn_few(c
         // P^T as a B fragment (k: slots, n: rows)
         const uint32_t pb0 = transpose8(pack_bf16(p[0], p[1]));
         const uint32_t pb1 = transpose8(pack_bf16(p[2], p[3]));
-        bool odd = false;  // a hidden slot's V may be an infinity or a NaN
         if (!kScaled && partly) {
+          // A hidden slot's V may be an infinity or a NaN, and 0 * NaN must not
+          // reach the rows that do not see it: such values are added to the rows
+          // that do, and the products go without them.
+          bool odd = false;
           const int c = lane % kPieces;
+          auto piece = [&](int i) {
+            return reinterpret_cast<uint4*>(ring + st * 2 * S::kHalf + S::kHalf +
+                                            swz<kPieces>(lane / kPieces + i * kPerPass, c));
+          };
 #pragma unroll
           for (int i = 0; i < 16 / kPerPass; ++i) {
-            const uint4 v = *reinterpret_cast<const uint4*>(
-                ring + st * 2 * S::kHalf + S::kHalf + swz<kPieces>(lane / kPieces + i * kPerPass, c));
-            const uint32_t y[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              odd = odd || (y[k] & 0x7F80u) == 0x7F80u || (y[k] & 0x7F800000u) == 0x7F800000u;
+            const uint4 v = *piece(i);
+            odd = odd || non_finite(v.x) || non_finite(v.y) || non_finite(v.z) || non_finite(v.w);
           }
-          odd = __any_sync(0xffffffffu, odd);
-        }
-        if (!odd) {
-          if constexpr (kScaled) {
+          if (__any_sync(0xffffffffu, odd)) {
+#pragma unroll 1
+            for (int j = 0; j < 16; ++j) {
+              const int from = (j & 7) * 4 + tq;
+              const float w0 = __shfl_sync(0xffffffffu, j < 8 ? p[0] : p[2], from);
+              const float w1 = __shfl_sync(0xffffffffu, j < 8 ? p[1] : p[3], from);
+              const uint32_t h = __shfl_sync(0xffffffffu, j < 8 ? hid : hid >> 2, from);
 #pragma unroll
-            for (int c = 0; c < D / 16; c += 2) {
-              uint32_t r[4];  // slots 0-7 and 8-15 of piece c, then of piece c + 1
-              ldsm4t(r, tv + swz<kPieces>((mi & 1) * 8 + mr, c + (mi >> 1)));
+              for (int cc = 0; cc < D / 16; ++cc)
 #pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const uint32_t va[4] = {widen2<kBytes02>(r[2 * u]), widen2<kBytes13>(r[2 * u]),
-                                        widen2<kBytes02>(r[2 * u + 1]), widen2<kBytes13>(r[2 * u + 1])};
-                mma16816(o[c + u], va, pb0, pb1);
-              }
+                for (int e = 0; e < 2; ++e) {
+                  const uint32_t x = (uint32_t) * reinterpret_cast<const uint16_t*>(
+                      ring + st * 2 * S::kHalf + S::kHalf + swz<kPieces>(j, (2 * cc + e) % kPieces) +
+                      2 * g) << 16;
+                  if ((x & 0x7F800000u) == 0x7F800000u) {
+                    if (!(h & 1)) o[cc][2 * e] = fmaf(w0, __uint_as_float(x), o[cc][2 * e]);
+                    if (!(h & 2)) o[cc][2 * e + 1] = fmaf(w1, __uint_as_float(x), o[cc][2 * e + 1]);
+                  }
+                }
             }
-          } else {
+            __syncwarp();
 #pragma unroll
-            for (int c = 0; c < D / 16; ++c) {
-              uint32_t r[4];  // dims 0-7 and 8-15 of slots 0-7, then of slots 8-15
-              ldsm4t(r, tv + swz<kPieces>((mi >> 1) * 8 + mr, 2 * c + (mi & 1)));
-              mma16816(o[c], r, pb0, pb1);
+            for (int i = 0; i < 16 / kPerPass; ++i) {
+              const uint4 v = *piece(i);
+              *piece(i) = make_uint4(without_non_finite(v.x), without_non_finite(v.y),
+                                     without_non_finite(v.z), without_non_finite(v.w));
+            }
+            __syncwarp();
+          }
+        }
+        if constexpr (kScaled) {
+#pragma unroll
+          for (int c = 0; c < D / 16; c += 2) {
+            uint32_t r[4];  // slots 0-7 and 8-15 of piece c, then of piece c + 1
+            ldsm4t(r, tv + swz<kPieces>((mi & 1) * 8 + mr, c + (mi >> 1)));
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const uint32_t va[4] = {widen2<kBytes02>(r[2 * u]), widen2<kBytes13>(r[2 * u]),
+                                      widen2<kBytes02>(r[2 * u + 1]), widen2<kBytes13>(r[2 * u + 1])};
+              mma16816(o[c + u], va, pb0, pb1);
             }
           }
         } else {
-          // out of the ordinary: 0 * NaN must not reach the rows that do not
-          // see the slot, so P V by scalars over the slots that a row sees
-#pragma unroll 1
-          for (int j = 0; j < 16; ++j) {
-            const int from = (j & 7) * 4 + tq;
-            const float w0 = __shfl_sync(0xffffffffu, j < 8 ? p[0] : p[2], from);
-            const float w1 = __shfl_sync(0xffffffffu, j < 8 ? p[1] : p[3], from);
-            const uint32_t h = __shfl_sync(0xffffffffu, j < 8 ? hid : hid >> 2, from);
 #pragma unroll
-            for (int c = 0; c < D / 16; ++c)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const uint16_t v = *reinterpret_cast<const uint16_t*>(
-                    ring + st * 2 * S::kHalf + S::kHalf + swz<kPieces>(j, (2 * c + e) % kPieces) + 2 * g);
-                const float x = __uint_as_float((uint32_t)v << 16);
-                if (!(h & 1)) o[c][2 * e] = fmaf(w0, x, o[c][2 * e]);
-                if (!(h & 2)) o[c][2 * e + 1] = fmaf(w1, x, o[c][2 * e + 1]);
-              }
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t r[4];  // dims 0-7 and 8-15 of slots 0-7, then of slots 8-15
+            ldsm4t(r, tv + swz<kPieces>((mi >> 1) * 8 + mr, 2 * c + (mi & 1)));
+            mma16816(o[c], r, pb0, pb1);
           }
         }
       }

@@ -149,15 +149,6 @@ __device__ __forceinline__ uint32_t ldg1(const uint8_t* p, bool on) {
 __device__ __forceinline__ uint32_t piece_at(int r, int c) {
   return (uint32_t)((c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
-__device__ __forceinline__ bool non_finite(uint32_t two) {  // of a bf16 pair
-  return (two & 0x7F80u) == 0x7F80u || (two & 0x7F800000u) == 0x7F800000u;
-}
-__device__ __forceinline__ uint32_t without_non_finite(uint32_t two) {
-  if ((two & 0x7F80u) == 0x7F80u) two &= 0xFFFF0000u;
-  if ((two & 0x7F800000u) == 0x7F800000u) two &= 0x0000FFFFu;
-  return two;
-}
-
 // A row scale 2^(byte - 127) as two bf16 factors for the bits of e4m3 on their
 // way to bf16 (the seven magnitude bits at the bottom of the exponent: the value
 // times 2^-120): 2^(byte - 7), 2^127 at most, in the lower half; the rest, 1 but
@@ -885,6 +876,8 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
         tc_fence_before();
         named_barrier_sync(1, 256);  // O and xml are read out
       }
+      // a warpgroup without rows does not run ahead: its arrivals belong to units
+      if (!kAlt && x.rows <= 128) named_barrier_sync(1, 256);
       __syncwarp();
       if (lane == 0) mbar_arrive(UE(units & 1));
       tiles += T;
