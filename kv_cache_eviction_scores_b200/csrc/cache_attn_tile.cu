@@ -12,14 +12,16 @@
 //
 // Layout: a unit of 256 rows is two query tiles of 128 rows against tiles of
 // 128 slots; a staged K/V tile serves both, so the staging (four producer
-// warps: page lookups, asynchronous 16-byte copies or, for e4m3, loads, the
+// warps there: page lookups, asynchronous 16-byte copies or, for e4m3, loads, the
 // widening and stores) is paid once per 256 rows.  Per query tile u: S_u = Q_u
 // K^T (M = N = 128) in TMEM columns 128 u, P_u over it (each half of P over the
 // half of S that it comes from), O_u at 256 + 128 u, all 512 columns.  One softmax warpgroup per query tile; while
 // one tile's softmax runs, the other tile's MMAs fill the tensor pipe.  P V of
 // a tile begins when the upper half of P is there.
-// kAlt (units of at most 128 rows): one query tile, and the two warpgroups take
-// the slot tiles in turn, each with its own S/P and O, joined at a unit's end.
+// kAlt (units of at most 128 rows, which read more than they compute): one query
+// tile, one softmax warpgroup and eight producer warps; S of the next slot tile
+// goes to the other of two S/P buffers while this one's softmax runs, so that the
+// softmax waits for no product.
 //
 // Every role walks the CTA's range by itself, so that staging runs on into the
 // next unit while the last one is finished.  A slot without a page and the
@@ -30,6 +32,8 @@
 //
 // Every wait on an mbarrier is bounded (some two seconds); on expiry the
 // kernel records DROPKV_ERR_TIMEOUT, every role leaves, and TMEM is freed.
+#include <type_traits>
+
 #include "cache_attn.cuh"
 #include "tc_ptx.cuh"
 
@@ -39,15 +43,16 @@ namespace {
 
 using namespace tc;
 
-constexpr int kTThreads = 448, kTTile = 128, kTCtas = 148;
-constexpr int kTProd = 4;                    // producer warps 8..11
-constexpr int kTMmaWarp = 12;                // 12 and 13: one per query tile (kAlt: per warpgroup)
+constexpr int kTTile = 128, kTCtas = 148;
+constexpr int kTMmaWarp = 12;  // the softmax warps, the producers, then the MMA issuers
 constexpr long long kTWaitClocks = 4000000000ll;  // of a wait: two seconds at least
 constexpr uint32_t kTColO = 256;
 
 
 template <typename TP, int D, bool kAlt>
 struct TileShared {
+  static constexpr int kSoftmax = kAlt ? 4 : 8, kProd = kTMmaWarp - kSoftmax;  // warps
+  static constexpr int kThreads = 32 * (kTMmaWarp + (kAlt ? 1 : 2));
   static constexpr bool kScaled = sizeof(TP) == 1;
   static constexpr int kStages = kAlt && !kScaled ? 3 : 2;
   static constexpr int kRing = !kScaled ? 0 : kAlt ? 4 : 2;  // e4m3 K or V tiles on their way
@@ -59,11 +64,10 @@ struct TileShared {
   static constexpr int oV = oK + kStages * kTileBytes;
   static constexpr int oRaw = oV + kStages * kTileBytes;
   static constexpr int oBars = oRaw + kRing * 128 * D;
-  static constexpr int oMask = oBars + (kBars + 1) / 2 * 16;  // uint32 [8][4]
+  static constexpr int oMask = oBars + (kBars + 1) / 2 * 16;  // [8][kProd] words of a bit a slot, 16 bytes a tile
   static constexpr int oOdd = oMask + 128;                    // int [2]
   static constexpr int oMisc = oOdd + 16;                     // TMEM base
-  static constexpr int oXml = oMisc + 16;                     // float2 [2][128], kAlt
-  static constexpr int oPlan = oXml + (kAlt ? 2 * 128 * 8 : 0);
+  static constexpr int oPlan = oMisc + 16;
   static constexpr int kBytes = oPlan + (int)sizeof(AttnPlanShared);
 };
 
@@ -245,11 +249,12 @@ __device__ __forceinline__ void add_non_finite(const AttnDev& a, int b, int h, i
 }
 
 template <typename TP, int D, bool kAlt>
-__global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
+__global__ void __launch_bounds__(TileShared<TP, D, kAlt>::kThreads, 1) k_attn_tile(const AttnDev a) {
   using S = TileShared<TP, D, kAlt>;
   constexpr int kStages = S::kStages, kRows = kAlt ? 128 : 256;
   constexpr bool kScaled = sizeof(TP) == 1;
   constexpr int kPieces = D / 8;  // of a staged row
+  constexpr int kProd = S::kProd, kMine = 128 / kProd;  // producers, rows of a tile of each
   // Of 8 exponentials, those on the FMA pipe (the special-function unit does 16 a
   // clock), and the half of P whose end starts the second query tile.  Measured
   // (512 tokens over 32K bf16 slots; 4 x 2048 over e4m3, whose widening fills the
@@ -265,12 +270,13 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
   }
   AttnPlanShared& plan = *reinterpret_cast<AttnPlanShared*>(sm + S::oPlan);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + S::oMisc);
-  volatile uint32_t* smask = reinterpret_cast<volatile uint32_t*>(sm + S::oMask);
+  using Bits = typename std::conditional<kAlt, uint16_t, uint32_t>::type;  // of a producer's slots
+  volatile Bits* smask = reinterpret_cast<volatile Bits*>(sm + S::oMask);
   volatile int* sodd = reinterpret_cast<volatile int*>(sm + S::oOdd);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto bar = [&](int i) { return base + S::oBars + 8 * i; };
   // Q full / empty; K and V full / empty per stage; per query tile (or, kAlt,
-  // warpgroup): S there, P's upper and lower half there, P V done
+  // S/P buffer): S there, P's upper and lower half there, P V done
   const uint32_t QF = bar(0), QE = bar(1);
   auto KF = [&](int s) { return bar(2 + s); };
   auto KE = [&](int s) { return bar(2 + kStages + s); };
@@ -287,12 +293,12 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
   const uint32_t GO = bar(kB0 + 10);
   if (threadIdx.x == 0) {
     mbar_init(GO, 1);
-    mbar_init(QF, kTProd);
-    mbar_init(QE, 2);
+    mbar_init(QF, kProd);
+    mbar_init(QE, kAlt ? 1 : 2);
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(KF(s), kTProd);
+      mbar_init(KF(s), kProd);
       mbar_init(KE(s), kAlt ? 1 : 2);
-      mbar_init(VF(s), kTProd);
+      mbar_init(VF(s), kProd);
       mbar_init(VE(s), kAlt ? 1 : 2);
     }
     for (int u = 0; u < 2; ++u) {
@@ -300,7 +306,7 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
       mbar_init(PA(u), 4);
       mbar_init(PB(u), 4);
       mbar_init(PD(u), 1);
-      mbar_init(UE(u), 8);
+      mbar_init(UE(u), S::kSoftmax);
       sodd[u] = 0;
     }
     fence_mbar_init();
@@ -311,26 +317,25 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
     tc_fence_before();
   }
   AttnWalk w;
-  bool more = attn_plan<kRows, kTTile, kTThreads>(a, plan, w);
+  bool more = attn_plan<kRows, kTTile, S::kThreads>(a, plan, w);
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
 
   if (warp >= kTMmaWarp) {
     // ---------------- MMA issuers ----------------
-    // Warp u: S and P V of query tile u (kAlt: of the slot tiles j = u mod 2), so
-    // that no tile's products wait for the other's softmax.  Measured against one
-    // warp for both, in turn or as they became ready: 331 against 350 and 377 us
-    // for 512 tokens over 32K bf16 slots (an MMA is issued as it executes, 64
-    // clocks, and a barrier seen some 100 clocks late).
+    // Warp u: S and P V of query tile u, so that no tile's products wait for the
+    // other's softmax.  Measured against one warp for both, in turn or as they
+    // became ready: 331 against 350 and 377 us for 512 tokens over 32K bf16 slots
+    // (an MMA is issued as it executes, 64 clocks, and a barrier seen some 100
+    // clocks late).  kAlt: one warp, S a tile ahead of P V.
     const int u = warp - kTMmaWarp;
-    constexpr int kStep = kAlt ? 2 : 1;
     constexpr uint32_t IDS = idesc_bf16(128, 128, false, false);  // S = Q K^T
     constexpr uint32_t IDP = idesc_bf16(128, D, false, true);     // O += P V (V MN-major)
-    const SDesc qd = sdesc_split(base + (kAlt ? 0 : u * S::kTileBytes), 16, 1024);
+    const SDesc qd = sdesc_split(base + u * S::kTileBytes, 16, 1024);
     const SDesc kd = sdesc_split(base + S::oK, 16, 1024);
     const SDesc vd = sdesc_split(base + S::oV, S::kBox, 1024);
-    const uint32_t dS = tbase + 128u * u, dO = tbase + kTColO + 128u * u;
+    const uint32_t dO = tbase + kTColO + 128u * u;
     uint32_t tiles = 0, units = 0;  // of the range so far
     uint32_t n = 0;                 // P V issued by this warp
     bool ok = true;
@@ -342,59 +347,64 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
       ok = warp_wait(QF, units & 1);
       ++units;
       tc_fence_after();
-      // S of tile j, once the P V that reads the last P from its columns is done
-      auto issue_S = [&](int j) {
+      // S, this warp's k-th, of tile j, once the P V that reads the last P from
+      // its columns (the buffer's last one) is done
+      auto issue_S = [&](int j, uint32_t k) {
         const uint32_t i = tiles + j, s = i % kStages;
+        const int f = kAlt ? k & 1 : u;
         if (!warp_wait(KF(s), (i / kStages) & 1)) return false;
-        if (n >= 1 && !warp_wait(PD(u), (n - 1) & 1)) return false;
+        if (kAlt ? k >= 2 && !warp_wait(PD(f), ((k >> 1) - 1) & 1)
+                 : k >= 1 && !warp_wait(PD(f), (k - 1) & 1))
+          return false;
         tc_fence_after();
         if (lane == 0) {
           const uint32_t klo = kd.lo + s * (S::kTileBytes >> 4);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t at = (uint32_t)((kk >> 2) * (S::kBox >> 4) + (kk & 3) * 2);
-            mma_ss_w(dS, qd.lo + at, qd.hi, klo + at, kd.hi, IDS, kk > 0 ? 1u : 0u);
+            mma_ss_w(tbase + 128u * f, qd.lo + at, qd.hi, klo + at, kd.hi, IDS, kk > 0 ? 1u : 0u);
           }
-          mma_commit(SF(u));
+          mma_commit(SF(f));
           mma_commit(KE(s));
           if (twice) mma_commit(KE(s));
-          if (j + kStep >= T) mma_commit(QE);
+          if (j == T - 1) mma_commit(QE);
         }
         __syncwarp();
         return true;
       };
-      const int first = kAlt ? u : 0;
-      if (kAlt ? first < T : 128 * u < x.rows) {
+      if (kAlt || 128 * u < x.rows) {
         // The second query tile begins half a tile late: in step, the two would
         // take turns to leave the tensor pipe and the special-function unit idle.
         if (!kAlt && u == 1) ok = ok && warp_wait(GO, (units - 1) & 1);
-        ok = ok && issue_S(first);
-        for (int j = first; j < T && ok; j += kStep) {
+        ok = ok && issue_S(0, n);
+        for (int j = 0; j < T && ok; ++j) {
+          if (kAlt && j + 1 < T) ok = issue_S(j + 1, n + 1);
           // O (+)= P V of tile j, as the halves of P come
           const uint32_t i = tiles + j, s = i % kStages;
           const uint32_t vlo = vd.lo + s * (S::kTileBytes >> 4);
-          ok = warp_wait(VF(s), (i / kStages) & 1);
+          const int f = kAlt ? n & 1 : u;
+          ok = ok && warp_wait(VF(s), (i / kStages) & 1);
 #pragma unroll
           for (int half = 1; half >= 0; --half) {
-            ok = ok && warp_wait(half ? PA(u) : PB(u), n & 1);
+            ok = ok && warp_wait(half ? PA(f) : PB(f), (kAlt ? n >> 1 : n) & 1);
             if (!ok) break;
             tc_fence_after();
             if (lane == 0) {
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)  // V slices of 16 rows, 2 KB
-                mma_ts_w(dO, dS + 64u * half + 8u * kk, vlo + 128u * (4 * half + kk), vd.hi, IDP,
-                         (j != first || half == 0 || kk > 0) ? 1u : 0u);
+                mma_ts_w(dO, tbase + 128u * f + 64u * half + 8u * kk, vlo + 128u * (4 * half + kk),
+                         vd.hi, IDP, (j > 0 || half == 0 || kk > 0) ? 1u : 0u);
             }
           }
           if (!ok) break;
           if (lane == 0) {
-            mma_commit(PD(u));
+            mma_commit(PD(f));
             mma_commit(VE(s));
             if (twice) mma_commit(VE(s));
           }
           __syncwarp();
           ++n;
-          if (j + kStep < T) ok = issue_S(j + kStep);
+          if (!kAlt && j + 1 < T) ok = issue_S(j + 1, n);
         }
       } else if (lane == 0) {
         mbar_arrive(QE);  // nothing to read; but no unit passes without this warp
@@ -403,11 +413,12 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
       more = attn_next<kRows, kTTile>(a, w);
     }
     if (!ok && lane == 0) fail(a);
-  } else if (warp >= 8) {
+  } else if (warp >= S::kSoftmax) {
     // ---------------- producers ----------------
-    // Warp pw stages the slots 32 pw .. 32 pw + 31 of every tile, and the
-    // query rows 32 pw ..; lane i looks up slot i.
-    const int pw = warp - 8;
+    // Warp pw stages the kMine slots from kMine pw on of every tile, and so the
+    // query rows; lane i looks up slot i mod kMine.
+    const int pw = warp - S::kSoftmax, row0 = pw * kMine;
+    const int mine = lane % kMine;
     uint32_t tc_ = 0, units = 0;  // tiles and units so far
     bool ok = true;
     const uint8_t* kp = reinterpret_cast<const uint8_t*>(a.c.k);
@@ -423,8 +434,8 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
       const int c = lane % kPieces;
       for (int q = 0; q < S::kQTiles; ++q) {
 #pragma unroll 4
-        for (int i = 0; i < 32 / kPer; ++i) {
-          const int r = pw * 32 + i * kPer + lane / kPieces, ur = q * 128 + r;
+        for (int i = 0; i < kMine / kPer; ++i) {
+          const int r = row0 + i * kPer + lane / kPieces, ur = q * 128 + r;
           const bool on = ur < x.rows;
           const AttnRow y = attn_row(a, x.b, w.h, x.rt * kRows + (on ? ur : 0));
           const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(a.q) + y.b * a.qs[0] +
@@ -441,7 +452,7 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
       const Unit x = unit_of<kRows>(a, w);
       // lane's slot of tile t, and the word of the tile's slots that are there
       auto look = [&](int t) {
-        return look_up(a, x.b, t < w.t1 ? t * kTTile + pw * 32 + lane : x.seen_all, x.seen_all);
+        return look_up(a, x.b, t < w.t1 ? t * kTTile + row0 + mine : x.seen_all, x.seen_all);
       };
       auto odd = [&]() { sodd[units & 1] = (int)units + 1; };
       Look nxt = look(w.t0);
@@ -452,8 +463,8 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
         auto clean = [&](int t, uint32_t s) {
           if ((t + 1) * kTTile <= x.seen_min) return;
           bool any = false;
-          for (int i = 0; i < 32 / kPer; ++i) {
-            const int r = pw * 32 + i * kPer + lane / kPieces;
+          for (int i = 0; i < kMine / kPer; ++i) {
+            const int r = row0 + i * kPer + lane / kPieces;
             if (t * kTTile + r < x.seen_min) continue;
             const uint32_t at = base + S::oV + s * S::kTileBytes + piece_at(r, c);
             uint4 v = lds16(at);
@@ -473,12 +484,12 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
           // K of this tile, then the last tile's V is handed over; V, then K
           ok = warp_wait(KE(s), ph ^ 1);
           if (!ok) break;
-          if (lane == 0) smask[(tc_ & 7) * 4 + pw] = word;
+          if (lane == 0) smask[(tc_ & 7) * kProd + pw] = (Bits)word;
           auto issue = [&](const uint8_t* pool, uint32_t dst) {
 #pragma unroll 4
-            for (int i = 0; i < 32 / kPer; ++i) {
+            for (int i = 0; i < kMine / kPer; ++i) {
               const int at = __shfl_sync(0xffffffffu, row, i * kPer + lane / kPieces);
-              copy16(dst + piece_at(pw * 32 + i * kPer + lane / kPieces, c),
+              copy16(dst + piece_at(row0 + i * kPer + lane / kPieces, c),
                      pool + (at < 0 ? 0 : (size_t)at * (D * 2) + c * 16), at >= 0);
             }
             copy_commit();
@@ -515,13 +526,13 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
         }
       } else {
         // a row of D bytes is D / 16 loads; a warp's pass covers kPer rows
-        constexpr int kIn = D / 16, kPer = 32 / kIn, kPass = 32 / kPer;
+        constexpr int kIn = D / 16, kPer = 32 / kIn, kPass = kMine / kPer;
         const int c = lane % kIn;
         // Jobs: K and V of a tile in turn, by the same code (one copy of it: see
         // the softmax's loops).  A ring holds the next kRing jobs' bytes as the
         // asynchronous copies land; a lane widens what it has copied.
         constexpr int kRing = S::kRing, kAhead = kRing / 2;  // jobs, tiles
-        const uint32_t ring = base + S::oRaw + pw * (32 * D) + lane * 16;
+        const uint32_t ring = base + S::oRaw + pw * (kMine * D) + lane * 16;
         auto issue = [&](int job, int row) {
           if (job < 2 * w.t1) {
             const uint8_t* pool = (job & 1 ? vp : kp) + c * 16;
@@ -540,7 +551,7 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
         auto put = [&](const uint32_t (&y)[8], int i, uint32_t dst) {
           // lanes of the second box store their odd piece first: eight lanes of a
           // row then hit eight different 16-byte bank groups
-          const int r = pw * 32 + i * kPer + lane / kIn;
+          const int r = row0 + i * kPer + lane / kIn;
           const bool swap = D == 128 && c >= kIn / 2;
           const uint4 p0 = make_uint4(y[0], y[1], y[2], y[3]), p1 = make_uint4(y[4], y[5], y[6], y[7]);
           sts16(dst + piece_at(r, 2 * c + swap), swap ? p1 : p0);
@@ -556,20 +567,21 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
           }
         };
         auto store = [&](uint32_t src, uint32_t byte, uint32_t dst, int part) {
+          constexpr int kBatch = kPass < 4 ? kPass : 4;
           const uint32_t own = widen_factors(byte);
-          // four passes' loads before their conversions: a warp alone on its
+          // some passes' loads before their conversions: a warp alone on its
           // scheduler has nobody else to hide their latency
 #pragma unroll 1
-          for (int i0 = 0; i0 < kPass; i0 += 4) {
-            uint4 in[4];
-            uint32_t f[4];
+          for (int i0 = 0; i0 < kPass; i0 += kBatch) {
+            uint4 in[kBatch];
+            uint32_t f[kBatch];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kBatch; ++i) {
               in[i] = lds16(src + (i0 + i) * 512);
               f[i] = __shfl_sync(0xffffffffu, own, (i0 + i) * kPer + lane / kIn);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kBatch; ++i) {
               uint32_t y[8];
               widen(in[i], f[i], y);
               put(y, i0 + i, dst);
@@ -581,8 +593,8 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
           bool any = false;
 #pragma unroll 1
           for (int i = 0; i < kPass; ++i) {
-            const int r = pw * 32 + i * kPer + lane / kIn;
-            const uint32_t f = __byte_perm(__shfl_sync(0xffffffffu, own, r & 31), 0, 0x3232);
+            const int r = row0 + i * kPer + lane / kIn;
+            const uint32_t f = __byte_perm(__shfl_sync(0xffffffffu, own, r - row0), 0, 0x3232);
 #pragma unroll 1
             for (int e = 0; e < 2; ++e) {
               const uint32_t at = dst + piece_at(r, 2 * c + e);
@@ -628,7 +640,7 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
           }
           ok = warp_wait(v ? VE(s) : KE(s), ph ^ 1);
           if (!ok) break;
-          if (!v && lane == 0) smask[(tc_ & 7) * 4 + pw] = words[0];
+          if (!v && lane == 0) smask[(tc_ & 7) * kProd + pw] = (Bits)words[0];
           copy_wait<kRing - 1>();
           store(ring + (uint32_t)(job % kRing) * (128 * D), v ? bv : bk,
                 base + (v ? S::oV : S::oK) + s * S::kTileBytes,
@@ -660,15 +672,12 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
   } else {
     // ---------------- softmax ----------------
     const int u = warp >> 2, ql = warp & 3;
-    const int row = ql * 32 + lane;                  // row of the query tile
-    const int crow = kAlt ? row : 128 * u + row;     // row of the unit
+    const int crow = 128 * u + ql * 32 + lane;       // row of the unit
     const uint32_t lane_off = (uint32_t)(ql * 32) << 16;
-    const uint32_t tS = tbase + 128u * u + lane_off;
     const uint32_t tO = tbase + kTColO + 128u * u + lane_off;
     const float c = a.c_log2;
     const uint64_t c2 = pk2(c, c);
-    uint32_t n = 0;              // slot tiles of this warpgroup so far
-    uint32_t other = 0;          // kAlt: of the other one
+    uint32_t n = 0;              // slot tiles of this query tile so far
     uint32_t tiles = 0, units = 0;
     bool live = true;            // no wait has run out
     auto alive = [&](bool got) {
@@ -680,19 +689,22 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
     while (more) {
       const Unit x = unit_of<kRows>(a, w);
       const int T = w.t1 - w.t0;
-      const bool warp_rows = (kAlt ? 0 : 128 * u) + ql * 32 < x.rows;
+      const bool warp_rows = 128 * u + ql * 32 < x.rows;
       const bool has = crow < x.rows;
       const int r = x.rt * kRows + crow;
       const int seen = has ? attn_seen(a, x.L, x.n, r) : 0;
       float m = -CUDART_INF_F, l = 0.f;
-      const bool mine = kAlt || 128 * u < x.rows;  // this query tile exists
-      for (int j = kAlt ? u : 0; j < T && live && mine; j += kAlt ? 2 : 1) {
-        alive(warp_wait(SF(u), n & 1));
+      const bool mine = 128 * u < x.rows;  // this query tile exists
+      for (int j = 0; j < T && live && mine; ++j) {
+        const int f = kAlt ? n & 1 : u;  // S/P buffer
+        const uint32_t tS = tbase + 128u * f + lane_off;
+        alive(warp_wait(SF(f), (kAlt ? n >> 1 : n) & 1));
         if (!live) break;
         if (warp_rows) {
           tc_fence_after();
           const int tok0 = (w.t0 + j) * kTTile, lim = seen - tok0;
-          const volatile uint32_t* mw = smask + ((tiles + j) & 7) * 4;
+          const volatile uint32_t* mw =
+              reinterpret_cast<volatile uint32_t*>(sm + S::oMask) + ((tiles + j) & 7) * 4;
           if (tok0 + kTTile > x.seen_min || (mw[0] & mw[1] & mw[2] & mw[3]) != ~0u) {
             // hidden slots: -inf over their logits
 #pragma unroll 1
@@ -730,8 +742,8 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
             l *= fac;
           }
           // rows whose reference moved: O, complete up to the last tile, by fac
-          if (__any_sync(0xffffffffu, fac != 1.f) && j >= (kAlt ? 2 : 1)) {
-            if (!warp_wait(PD(u), (n - 1) & 1)) {
+          if (__any_sync(0xffffffffu, fac != 1.f) && j >= 1) {
+            if (!warp_wait(PD(kAlt ? f ^ 1 : u), (kAlt ? (n - 1) >> 1 : n - 1) & 1)) {
               alive(false);
               break;
             }
@@ -772,7 +784,7 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(half ? PA(u) : PB(u));
+            if (lane == 0) mbar_arrive(half ? PA(f) : PB(f));
             if (!kAlt && half == kGoHalf && j == 0 && threadIdx.x == 0) mbar_arrive(GO);
           }
           float la, lb;
@@ -782,8 +794,8 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(PA(u));
-            mbar_arrive(PB(u));
+            mbar_arrive(PA(f));
+            mbar_arrive(PB(f));
           }
         }
         ++n;
@@ -821,61 +833,21 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tile(const AttnDev a) {
         else
           *reinterpret_cast<float2*>(part + a.pstride - 4) = make_float2(mm, ll);
       };
-      if constexpr (!kAlt) {
-        if (mine && live) alive(warp_wait(PD(u), (n - 1) & 1));
-        if (mine && live && warp_rows) {
-          tc_fence_after();
-          const bool fix = sodd[units & 1] == (int)units + 1;
-          const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll 1
-          for (int k = 0; k < D / 32; ++k) {
-            uint32_t o[32];
-            tmem_ld32(tO + 32u * k, o);
-            finish(o, 32 * k, fix, inv);
-          }
-          put_stats(m, l);
-        }
-        tc_fence_before();
-      } else {
-        // both warpgroups' rows, each half of the columns
-        float2* xml = reinterpret_cast<float2*>(sm + S::oXml);
-        other += u == 0 ? (uint32_t)(T / 2) : (uint32_t)((T + 1) / 2);
-        if (live && n > 0) alive(warp_wait(PD(u), (n - 1) & 1));
-        if (live && other > 0) alive(warp_wait(PD(u ^ 1), (other - 1) & 1));
-        xml[u * 128 + row] = make_float2(m, l);
-        named_barrier_sync(1, 256);
+      if (mine && live)
+        alive(warp_wait(PD(kAlt ? (n - 1) & 1 : u), (kAlt ? (n - 1) >> 1 : n - 1) & 1));
+      if (mine && live && warp_rows) {
         tc_fence_after();
-        if (live && warp_rows) {
-          const float2 a0 = xml[row], a1 = xml[128 + row];
-          const float M = fmaxf(a0.x, a1.x);
-          auto weight = [&](float2 y) {
-            return y.x == -CUDART_INF_F ? (y.y == 0.f ? 0.f : y.y) : attn_ex2(y.x - M);
-          };
-          const float f0 = weight(a0), f1 = weight(a1);
-          auto part_of = [&](float2 y, float f) { return y.x == -CUDART_INF_F ? y.y : y.y * f; };
-          const float ll = part_of(a0, f0) + part_of(a1, f1);
-          const bool fix = sodd[units & 1] == (int)units + 1;
-          const float inv = ll == 0.f ? 0.f : 1.f / ll;
-          const uint32_t t0 = tbase + kTColO + lane_off;
+        const bool fix = sodd[units & 1] == (int)units + 1;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
-          for (int k = u * (D / 64); k < (u + 1) * (D / 64); ++k) {
-            uint32_t o[32];
-            tmem_ld32(t0 + 32u * k, o);
-#pragma unroll
-            for (int y = 0; y < 32; ++y) o[y] = u32(f32(o[y]) * f0);
-            if (T > 1) {
-              uint32_t o1[32];
-              tmem_ld32(t0 + 128u + 32u * k, o1);
-#pragma unroll
-              for (int y = 0; y < 32; ++y) o[y] = u32(fmaf(f32(o1[y]), f1, f32(o[y])));
-            }
-            finish(o, 32 * k, fix, inv);
-          }
-          if (u == 0) put_stats(M, ll);
+        for (int k = 0; k < D / 32; ++k) {
+          uint32_t o[32];
+          tmem_ld32(tO + 32u * k, o);
+          finish(o, 32 * k, fix, inv);
         }
-        tc_fence_before();
-        named_barrier_sync(1, 256);  // O and xml are read out
+        put_stats(m, l);
       }
+      tc_fence_before();
       // a warpgroup without rows does not run ahead: its arrivals belong to units
       if (!kAlt && x.rows <= 128) named_barrier_sync(1, 256);
       __syncwarp();
@@ -900,7 +872,7 @@ cudaError_t launch_tile(const AttnDev& a, cudaStream_t st) {
   static_assert(smem <= 232448, "shared memory of a CTA");
   cudaError_t e = allow_smem<k_attn_tile<TP, D, kAlt>>(smem);
   if (e != cudaSuccess) return e;
-  kern<<<kTCtas, kTThreads, smem, st>>>(a);
+  kern<<<kTCtas, TileShared<TP, D, kAlt>::kThreads, smem, st>>>(a);
   return cudaGetLastError();
 }
 
