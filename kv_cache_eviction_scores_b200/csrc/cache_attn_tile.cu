@@ -161,30 +161,6 @@ __device__ __forceinline__ uint32_t widen_factors(uint32_t byte) {
   if (byte == 255u) return 0x3F807FC0u;
   return ((min(byte, 134u) + 120u) << 7) | (byte <= 134u ? 0x3F80u : (byte - 134u + 127u) << 7) << 16;
 }
-// 2^x of two values without the special-function unit: n = x rounded to an
-// integer by the addition of 1.5 2^23, 2^(x - n) on [-1/2, 1/2] by a polynomial of
-// degree 4 fitted for the least relative error (2.9e-6) under p(0) = 1, and n
-// added to the exponent.  x is clamped at -127, which gives exactly 0 there.
-__device__ __forceinline__ void ex2_poly2(float& x0, float& x1) {
-  const uint64_t x = pk2(fmaxf(x0, -127.f), fmaxf(x1, -127.f));
-  const uint64_t t = fadd2(x, pk2(12582912.f, 12582912.f));
-  const uint64_t f = ffma2(fadd2(t, pk2(-12582912.f, -12582912.f)), pk2(-1.f, -1.f), x);
-  uint64_t p = ffma2(pk2(0.009582852f, 0.009582852f), f, pk2(0.055906426f, 0.055906426f));
-  p = ffma2(p, f, pk2(0.24024099f, 0.24024099f));
-  p = ffma2(p, f, pk2(0.6931242f, 0.6931242f));
-  p = ffma2(p, f, pk2(1.f, 1.f));
-  float t0, t1, p0, p1;
-  upk2(t, t0, t1);
-  upk2(p, p0, p1);
-  x0 = f32(u32(p0) + (u32(t0) << 23));
-  x1 = f32(u32(p1) + (u32(t1) << 23));
-}
-__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {  // NaN if one of them is
-  float d;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-
 // The rows of one unit as a role sees them.
 struct Unit {
   int b, rt, rows, seen_all, seen_min, L, n;
@@ -255,12 +231,12 @@ __global__ void __launch_bounds__(TileShared<TP, D, kAlt>::kThreads, 1) k_attn_t
   constexpr bool kScaled = sizeof(TP) == 1;
   constexpr int kPieces = D / 8;  // of a staged row
   constexpr int kProd = S::kProd, kMine = 128 / kProd;  // producers, rows of a tile of each
-  // Of 8 exponentials, those on the FMA pipe (the special-function unit does 16 a
-  // clock), and the half of P whose end starts the second query tile.  Measured
-  // (512 tokens over 32K bf16 slots; 4 x 2048 over e4m3, whose widening fills the
-  // ALU pipe): 0 to 4 of 8 352, 349, 331, 349, 353 and 821, 792, 806, 826, 847 us;
-  // no delay, upper half, lower half 331, 319, 309 and 791, 764, 808 us.
-  constexpr int kTPoly = kScaled ? 1 : 2, kGoHalf = kScaled ? 1 : 0;
+  // The half of P whose end starts the second query tile.  Measured (512 tokens
+  // over 32K bf16 slots; 4 x 2048 over e4m3): no delay, upper half, lower half 331,
+  // 319, 309 and 791, 764, 808 us.  (Exponentials in part on the FMA pipe, by a
+  // polynomial, gained nothing once S was read less: 311 us without, 314 and 319
+  // with a quarter and three eighths of them there.)
+  constexpr int kGoHalf = kScaled ? 1 : 0;
   extern __shared__ __align__(1024) uint8_t sm[];
   pdl_trigger();
   const uint32_t base = smem_u32(sm);
@@ -703,15 +679,15 @@ __global__ void __launch_bounds__(TileShared<TP, D, kAlt>::kThreads, 1) k_attn_t
         if (warp_rows) {
           tc_fence_after();
           const int tok0 = (w.t0 + j) * kTTile, lim = seen - tok0;
-          const volatile uint32_t* mw =
-              reinterpret_cast<volatile uint32_t*>(sm + S::oMask) + ((tiles + j) & 7) * 4;
-          if (tok0 + kTTile > x.seen_min || (mw[0] & mw[1] & mw[2] & mw[3]) != ~0u) {
+          const uint4 there = lds16(base + S::oMask + ((tiles + j) & 7) * 16);
+          if (tok0 + kTTile > x.seen_min || (there.x & there.y & there.z & there.w) != ~0u) {
             // hidden slots: -inf over their logits
 #pragma unroll 1
             for (int k = 0; k < 8; ++k) {
               uint32_t o[16];
               tmem_ld16(tS + 16u * k, o);
-              const uint32_t word = mw[k >> 1] >> (16 * (k & 1));
+              const uint32_t two = k < 2 ? there.x : k < 4 ? there.y : k < 6 ? there.z : there.w;
+              const uint32_t word = two >> (16 * (k & 1));
 #pragma unroll
               for (int y = 0; y < 16; ++y)
                 if (16 * k + y >= lim || !((word >> y) & 1)) o[y] = 0xFF800000u;
@@ -721,20 +697,19 @@ __global__ void __launch_bounds__(TileShared<TP, D, kAlt>::kThreads, 1) k_attn_t
           }
           // Rolled loops over the halves of the row: straight-line code for all
           // of it (with the producers' beside it) ran out of the instruction
-          // caches, which cost more than the second TMEM read of S.
+          // caches, which cost more than the second TMEM read of a half.
+          uint32_t sr[64];
           float ya = -CUDART_INF_F, yb = -CUDART_INF_F;
 #pragma unroll 1
           for (int half = 0; half < 2; ++half) {
-            uint32_t sr[64];
             tmem_ld64(tS + 64u * half, sr);
 #pragma unroll
             for (int k = 0; k < 64; k += 4) {
-              ya = fmax3_nan(ya, f32(sr[k]), f32(sr[k + 1]));
-              yb = fmax3_nan(yb, f32(sr[k + 2]), f32(sr[k + 3]));
+              ya = fmax3(ya, f32(sr[k]), f32(sr[k + 1]));
+              yb = fmax3(yb, f32(sr[k + 2]), f32(sr[k + 3]));
             }
           }
-          const float mt = fmax3_nan(ya, yb, -CUDART_INF_F) * c;  // c > 0
-          if (!(mt < CUDART_INF_F)) l = CUDART_NAN_F;  // so is the row, whatever becomes of P
+          const float mt = fmaxf(ya, yb) * c;  // c > 0
           float fac = 1.f;
           if (mt > m + 8.f) {
             fac = m == -CUDART_INF_F ? 0.f : attn_ex2(m - mt);
@@ -763,20 +738,13 @@ __global__ void __launch_bounds__(TileShared<TP, D, kAlt>::kThreads, 1) k_attn_t
           uint64_t l2 = pk2(l, 0.f);
 #pragma unroll 1
           for (int half = 1; half >= 0; --half) {
-            uint32_t sr[64];
-            tmem_ld64(tS + 64u * half, sr);
+            if (half == 0) tmem_ld64(tS, sr);  // the upper half is still there
             uint32_t pw[32];
 #pragma unroll
             for (int k = 0; k < 32; ++k) {
               float d0, d1;
               upk2(ffma2(pk2(f32(sr[2 * k]), f32(sr[2 * k + 1])), c2, nmu2), d0, d1);
-              float e0 = d0, e1 = d1;
-              if (k % 8 < kTPoly) {
-                ex2_poly2(e0, e1);
-              } else {
-                e0 = attn_ex2(d0);
-                e1 = attn_ex2(d1);
-              }
+              const float e0 = attn_ex2(d0), e1 = attn_ex2(d1);
               l2 = fadd2(l2, pk2(e0, e1));
               pw[k] = pack_bf16(e0, e1);
             }
