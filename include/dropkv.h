@@ -284,7 +284,9 @@ DROPKV_API dropkv_status dropkv_scores_select(const dropkv_shape* shape, const v
  * max |x| <= 448 * 2^e (a row of zeros: byte 0).  A power of two costs an 8-bit
  * float no precision, makes scaling exact in both directions, and makes the
  * stored bits independent of the arithmetic.  A row that holds an infinity or a
- * NaN is stored as byte 255 and reads back as NaN.
+ * NaN is stored as byte 255 and reads back as NaN.  (Pages that something else
+ * filled: attention takes a NaN from a row's scale byte only; a value's own NaN
+ * code beside a finite scale, which a write never leaves, may count as 480.)
  */
 typedef struct dropkv_cache {
   int32_t B;            /* sequences (rows of the page table), >= 1                 */
@@ -341,7 +343,10 @@ DROPKV_API dropkv_status dropkv_cache_read(const dropkv_cache* cache,
  *   out = softmax(scale q . k_j) v_j,   lse = log sum_j exp(scale q . k_j).
  * A row that sees nothing gets out = 0 and lse = -inf.  What a row does not see
  * has no influence on it, whatever it holds (NaN included).  Rows t >= n of out
- * and lse stay as they are.  Query head hq uses KV head hq / (Hq / Hkv). */
+ * and lse stay as they are.  Query head hq uses KV head hq / (Hq / Hkv).
+ * Arithmetic: fp32; on the TENSOR path q, k and v enter as bf16 and the weights
+ * that meet v are rounded to bf16.  *status_dev receives DROPKV_ERR_TIMEOUT if a
+ * wait inside a kernel gave up (its rows are then undefined). */
 typedef struct dropkv_cache_attn {
   const void* q;        /* device [B, Hq, T, d], strided (last index contiguous)    */
   void* out;            /* device [B, Hq, T, d], strided                            */

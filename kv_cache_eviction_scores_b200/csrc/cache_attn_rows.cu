@@ -1,5 +1,6 @@
 // cache_attn_rows.cu -- cache attention for few query rows per KV head
-// (decoding, short drafts): bf16 queries, bf16 or e4m3 pages, head dim 64/128.
+// (decoding, short drafts): bf16 queries, bf16 or e4m3 pages, head dim 64/128;
+// k_attn_few up to eight rows, k_attn_rows up to 16.
 //
 // Mathematics: the online softmax, per row with reference maximum m (log2
 // units) and sum l: P = 2^(c q.k_j - m), l += sum P, O += P V; the reference
@@ -506,7 +507,8 @@ __global__ void __launch_bounds__(kRThreads, 1) k_attn_rows(const AttnDev a) {
 // the kernel above, whose row block would be half empty; with e4m3 pages, whose
 // tiles are half the bytes, two CTAs then fit an SM, and their warps hide each
 // other's latencies, which bound that kernel there (64 sequences of 2K to 16K
-// e4m3 slots, 7 rows each: MEASURE_FEW).
+// e4m3 slots, 7 rows each: 207 us by 16 rows, 119 by eight; four 128K bf16
+// caches, 4 rows each, 320 and 318, 98 % of the measured copy bandwidth).
 template <typename TP, int D>
 struct FewShared {
   static constexpr int kDepth = 3;
