@@ -51,6 +51,12 @@ __device__ __forceinline__ void attn_lengths(const AttnDev& a, int b, int& L, in
     n = min(max(n, 0), a.T);
   }
 }
+// n / d of non-negative values, which mostly fit 32 bits: the 64-bit division is a
+// long routine, and the CTAs' ranges take several one after the other.
+__device__ __forceinline__ int64_t attn_div(int64_t n, int64_t d) {
+  if (((uint64_t)n | (uint64_t)d) >> 32) return n / d;
+  return (int64_t)((uint32_t)n / (uint32_t)d);
+}
 // Slots that row r (token r / G) sees.
 __device__ __forceinline__ int attn_seen(const AttnDev& a, int L, int n, int r) {
   return a.causal ? max(0, L - n + (int)a.fG.div((uint32_t)r) + 1) : L;
@@ -157,7 +163,7 @@ __device__ __forceinline__ bool attn_seek(const AttnDev& a, AttnPlanShared& sh, 
   w.item = sh.item;
   w.nt = sh.nt;
   const int64_t in_item = at - sh.g0;
-  w.h = (int)(in_item / w.nt);
+  w.h = (int)attn_div(in_item, w.nt);
   w.t0 = (int)(in_item - (int64_t)w.h * w.nt);
   w.g0 = sh.g0 + (int64_t)w.h * w.nt;
   return true;
@@ -169,7 +175,7 @@ __device__ __forceinline__ int attn_grid(int64_t total, int ctas) {
   return (int)min((int64_t)ctas, total);
 }
 __device__ __forceinline__ int64_t attn_range(int64_t total, int grid, int cta) {
-  return total * cta / grid;
+  return attn_div(total * cta, grid);
 }
 
 // The range of this CTA (kThreads threads, all call it).
@@ -229,6 +235,28 @@ __device__ __forceinline__ void attn_put_lse(const AttnDev& a, const AttnRow& x,
   if (a.lse)
     a.lse[((int64_t)x.b * a.Hq + x.hq) * a.T + x.t] =
         l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : (l == 0.f ? -CUDART_INF_F : l);
+}
+
+// The page and the offset in it of slot `slot` < end of the sequence with this
+// page table row; off -1: no slot.  Volatile: requested here, a tile before it is
+// used.
+struct Look {
+  int page, off;
+};
+__device__ __forceinline__ Look look_up(const AttnDev& a, const int32_t* table, int slot, int end) {
+  Look k = {-1, -1};
+  if (slot < end) {
+    const int pi = (int)a.c.fpage.div((uint32_t)slot);
+    asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(k.page) : "l"(table + pi));
+    k.off = slot - pi * a.c.page;
+  }
+  return k;
+}
+// Its pool row, or -1 (32 bits: the tensor path's host side checked the size).
+__device__ __forceinline__ int pool_row(const AttnDev& a, int h, Look k) {
+  if ((uint32_t)k.page < (uint32_t)a.c.n_pages) return (k.page * a.c.Hkv + h) * a.c.page + k.off;
+  if (k.off >= 0) raise_arg(a.status);
+  return -1;
 }
 
 struct AttnGrid {

@@ -167,24 +167,11 @@ __global__ void __launch_bounds__(kRThreads, 1) k_attn_rows(const AttnDev a) {
 
     // the page of this lane's slot (lane & 15) of tile t: looked up one step
     // before its copy is issued
-    int npage = -1, noff = 0;
     auto look = [&](int t) {
-      const int slot = t * kRTile + warp * 16 + (lane & 15);
-      npage = -1;
-      noff = 0;
-      if (t < w.t1 && slot < seen_all) {
-        const int pi = (int)a.c.fpage.div((uint32_t)slot);
-        npage = __ldg(table + pi);
-        noff = slot - pi * a.c.page;
-        if (npage == -1) npage = -2;  // a slot without a page, not the end of the tiles
-      }
+      return look_up(a, table, t * kRTile + warp * 16 + (lane & 15), t < w.t1 ? seen_all : 0);
     };
-    auto issue = [&](int st) {
-      int row = -1;
-      if ((uint32_t)npage < (uint32_t)a.c.n_pages)
-        row = (npage * a.c.Hkv + w.h) * a.c.page + noff;
-      else if (npage != -1)
-        raise_arg(a.status);
+    auto issue = [&](int st, const Look& at_) {
+      const int row = pool_row(a, w.h, at_);
       if (lane < 16) srow[warp][st][lane] = row;
       const uint32_t dk = ring_s + st * 2 * S::kHalf, dv = dk + S::kHalf;
       const int c = lane % kPieces;
@@ -197,12 +184,15 @@ __global__ void __launch_bounds__(kRThreads, 1) k_attn_rows(const AttnDev a) {
         copy16(dv + swz<kPieces>(r, c), vp + off, at >= 0);
       }
     };
-    look(w.t0);
+    // the first tiles' lookups travel together
+    Look first[kDepth - 1], nxt;
+#pragma unroll
+    for (int i = 0; i < kDepth - 1; ++i) first[i] = look(w.t0 + i);
+    nxt = look(w.t0 + kDepth - 1);
 #pragma unroll
     for (int i = 0; i < kDepth - 1; ++i) {
-      issue(i);
+      issue(i, first[i]);
       copy_commit();
-      look(w.t0 + i + 1);
     }
 
     // the two rows of this lane's quad, and their queries as A fragments
@@ -265,9 +255,9 @@ __global__ void __launch_bounds__(kRThreads, 1) k_attn_rows(const AttnDev a) {
       if (kScaled)
         sscale[warp][t & 1][lane >> 4][lane & 15] = scale_of(sbyte) * (lane < 16 ? a.c_log2 : 1.f);
       const int stn = st + kDepth - 1 >= kDepth ? st - 1 : st + kDepth - 1;
-      issue(stn);
+      issue(stn, nxt);
       copy_commit();
-      look(t + kDepth);
+      nxt = look(t + kDepth);
       __syncwarp();
       const int st1 = st + 1 == kDepth ? 0 : st + 1;
       if (kScaled && t + 1 < w.t1) scale_load(st1);
@@ -562,23 +552,12 @@ __global__ void __launch_bounds__(kRThreads, few_ctas_per_sm<TP>()) k_attn_few(c
     const int32_t* table = a.c.table + (size_t)b * a.c.max_pages;
 
     // the page of this lane's slot (lane & 15) of tile t: looked up one step
-    // before its copy is issued (volatile: requested here)
-    int npage = -1, noff = -1;
+    // before its copy is issued
     auto look = [&](int t) {
-      const int slot = t * kRTile + warp * 16 + (lane & 15);
-      npage = noff = -1;
-      if (t < w.t1 && slot < seen_all) {
-        const int pi = (int)a.c.fpage.div((uint32_t)slot);
-        asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(npage) : "l"(table + pi));
-        noff = slot - pi * a.c.page;
-      }
+      return look_up(a, table, t * kRTile + warp * 16 + (lane & 15), t < w.t1 ? seen_all : 0);
     };
-    auto issue = [&](int st) {
-      int row = -1;
-      if ((uint32_t)npage < (uint32_t)a.c.n_pages)
-        row = (npage * a.c.Hkv + w.h) * a.c.page + noff;
-      else if (noff >= 0)
-        raise_arg(a.status);
+    auto issue = [&](int st, const Look& at_) {
+      const int row = pool_row(a, w.h, at_);
       if (lane < 16) srow[warp][st][lane] = row;
       const uint32_t dk = ring_s + st * 2 * S::kHalf, dv = dk + S::kHalf;
       const int c = lane % kPieces;
@@ -591,12 +570,15 @@ __global__ void __launch_bounds__(kRThreads, few_ctas_per_sm<TP>()) k_attn_few(c
         copy16(dv + swz<kPieces>(r, c), vp + off, at >= 0);
       }
     };
-    look(w.t0);
+    // the first tiles' lookups travel together
+    Look first[kDepth - 1], nxt;
+#pragma unroll
+    for (int i = 0; i < kDepth - 1; ++i) first[i] = look(w.t0 + i);
+    nxt = look(w.t0 + kDepth - 1);
 #pragma unroll
     for (int i = 0; i < kDepth - 1; ++i) {
-      issue(i);
+      issue(i, first[i]);
       copy_commit();
-      look(w.t0 + i + 1);
     }
 
     // query row g as a B fragment (k: dims, n: rows), and the two rows whose
@@ -654,9 +636,9 @@ __global__ void __launch_bounds__(kRThreads, few_ctas_per_sm<TP>()) k_attn_few(c
       if (kScaled)
         sscale[warp][t & 1][lane >> 4][lane & 15] = scale_of(sbyte) * (lane < 16 ? a.c_log2 : 1.f);
       const int stn = st + kDepth - 1 >= kDepth ? st - 1 : st + kDepth - 1;
-      issue(stn);
+      issue(stn, nxt);
       copy_commit();
-      look(t + kDepth);
+      nxt = look(t + kDepth);
       __syncwarp();
       const int st1 = st + 1 == kDepth ? 0 : st + 1;
       if (kScaled && t + 1 < w.t1) scale_load(st1);

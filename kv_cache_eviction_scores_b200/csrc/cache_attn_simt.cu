@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(128) k_attn_merge(const AttnDev a, int ctas) {
     pdl_wait();
     return;
   }
-  const int c1 = (int)(((w.g0 + w.nt) * grid - 1) / total);  // the CTA of its last tile
+  const int c1 = (int)attn_div((w.g0 + w.nt) * grid - 1, total);  // the CTA of its last tile
   const int pieces = c1 - c0 + 1;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int b = w.item / a.nrt, rt = w.item - b * a.nrt;

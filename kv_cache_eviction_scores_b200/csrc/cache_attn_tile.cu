@@ -177,27 +177,6 @@ __device__ __forceinline__ Unit unit_of(const AttnDev& a, const AttnWalk& w) {
   return x;
 }
 
-// Pool row of slot `slot`, or -1 (32 bits: the host checked the pools' size).
-struct Look {
-  int page, off;  // off -1: no slot
-};
-__device__ __forceinline__ Look look_up(const AttnDev& a, int b, int slot, int end) {
-  Look k = {-1, -1};
-  if (slot < end) {
-    const int pi = (int)a.c.fpage.div((uint32_t)slot);
-    // volatile: requested here, a tile before it is used
-    asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(k.page)
-                 : "l"(a.c.table + (size_t)b * a.c.max_pages + pi));
-    k.off = slot - pi * a.c.page;
-  }
-  return k;
-}
-__device__ __forceinline__ int pool_row(const AttnDev& a, int h, Look k) {
-  if ((uint32_t)k.page < (uint32_t)a.c.n_pages) return (k.page * a.c.Hkv + h) * a.c.page + k.off;
-  if (k.off >= 0) raise_arg(a.status);
-  return -1;
-}
-
 // The infinities and NaNs of V that a row sees, of its unit's partly seen
 // slots: added to 32 columns of its O from column c0 on (rare).
 template <typename TP, int D>
@@ -426,9 +405,10 @@ __global__ void __launch_bounds__(TileShared<TP, D, kAlt>::kThreads, 1) k_attn_t
       ok = units < 2 || warp_wait(UE(units & 1), ((units >> 1) - 1) & 1);
       if (!ok) break;
       const Unit x = unit_of<kRows>(a, w);
+      const int32_t* table = a.c.table + (size_t)x.b * a.c.max_pages;
       // lane's slot of tile t, and the word of the tile's slots that are there
       auto look = [&](int t) {
-        return look_up(a, x.b, t < w.t1 ? t * kTTile + row0 + mine : x.seen_all, x.seen_all);
+        return look_up(a, table, t * kTTile + row0 + mine, t < w.t1 ? x.seen_all : 0);
       };
       auto odd = [&]() { sodd[units & 1] = (int)units + 1; };
       Look nxt = look(w.t0);
