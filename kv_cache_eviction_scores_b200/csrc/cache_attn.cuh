@@ -34,6 +34,14 @@ struct AttnDev {
   int32_t* status;
 };
 
+// An attention kernel's first step.  It may be launched while its predecessor in
+// the stream ends, and waits for that here; only then may the join be launched,
+// which reads the lengths before its own wait.
+__device__ __forceinline__ void attn_begin() {
+  pdl_wait();
+  pdl_trigger();
+}
+
 // ex2 and the row statistics are in units of log2.
 __device__ __forceinline__ float attn_ex2(float x) {
   float y;

@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kRThreads, 1) k_attn_rows(const AttnDev a) {
   __shared__ int srow[kRWarps][kDepth][16];       // pool rows of the ring's slots, -1: none
   __shared__ float sscale[kRWarps][2][2][16];     // K's scale times c_log2, V's scale
   __shared__ float2 sml[kRWarps][kRRows];
-  pdl_trigger();
+  attn_begin();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, tq = lane & 3;
   uint8_t* ring = sm + warp * kDepth * 2 * S::kHalf;
@@ -533,7 +533,7 @@ __global__ void __launch_bounds__(kRThreads, few_ctas_per_sm<TP>()) k_attn_few(c
   __shared__ int srow[kRWarps][kDepth][16];    // pool rows of the ring's slots, -1: none
   __shared__ float sscale[kRWarps][2][2][16];  // K's scale times c_log2, V's scale
   __shared__ float2 sml[kRWarps][kFRows];
-  pdl_trigger();
+  attn_begin();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, tq = lane & 3;
   uint8_t* ring = sm + warp * kDepth * 2 * S::kHalf;
@@ -852,8 +852,7 @@ cudaError_t launch_rows(const AttnDev& a, cudaStream_t st) {
   constexpr int smem = RowsShared<TP, D>::kBytes;
   cudaError_t e = allow_smem<k_attn_rows<TP, D>>(smem);
   if (e != cudaSuccess) return e;
-  kern<<<kRCtas, kRThreads, smem, st>>>(a);
-  return cudaGetLastError();
+  return launch_ex(kern, dim3(kRCtas), dim3(kRThreads), smem, st, true, 1, a);
 }
 
 template <typename TP, int D>
@@ -861,8 +860,8 @@ cudaError_t launch_few(const AttnDev& a, cudaStream_t st) {
   constexpr int smem = FewShared<TP, D>::kBytes;
   cudaError_t e = allow_smem<k_attn_few<TP, D>>(smem);
   if (e != cudaSuccess) return e;
-  k_attn_few<TP, D><<<kRCtas * few_ctas_per_sm<TP>(), kRThreads, smem, st>>>(a);
-  return cudaGetLastError();
+  return launch_ex(k_attn_few<TP, D>, dim3(kRCtas * few_ctas_per_sm<TP>()), dim3(kRThreads), smem, st,
+                   true, 1, a);
 }
 
 }  // namespace

@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kSThreads, 4) k_attn_simt(const AttnDev a) {
   extern __shared__ __align__(16) float sm[];
   __shared__ AttnPlanShared plan;
   __shared__ int64_t srow[2][kSTile];  // pool rows of a tile's slots, -1: none
-  pdl_trigger();
+  attn_begin();
   const int d = a.c.d, ds = row_stride(d);
   float* sQ = sm;
   float* sK = sQ + kSRows * ds;
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kSThreads, kCols > 4 ? 1 : kCols > 2 ? 2 : 3) 
   extern __shared__ __align__(16) float sm[];
   __shared__ AttnPlanShared plan;
   __shared__ int64_t srow[2][kSTile];  // pool rows of a tile's slots, -1: none
-  pdl_trigger();
+  attn_begin();
   const int d = a.c.d, ds = row_stride(d), d4 = (d + 3) & ~3;
   float* sQ = sm;
   float* sK = sQ + kLRows * ds;
@@ -506,6 +506,7 @@ template <typename TQ, int kRows, int kTile>
 __global__ void __launch_bounds__(128) k_attn_merge(const AttnDev a, int ctas) {
   constexpr int kFly = 12;
   __shared__ AttnPlanShared plan;
+  pdl_trigger();  // the next call's kernel waits for this one's end
   AttnWalk w;
   int64_t total, first = 0, last = 0;
   int grid = 0;
@@ -658,8 +659,7 @@ cudaError_t launch_simt(const AttnDev& a, cudaStream_t st) {
   const auto kern = k_attn_simt<TQ, TP>;
   cudaError_t e = allow_smem<k_attn_simt<TQ, TP>>((int)bytes(256));
   if (e != cudaSuccess) return e;
-  kern<<<kSCtas, kSThreads, smem, st>>>(a);
-  return cudaGetLastError();
+  return launch_ex(kern, dim3(kSCtas), dim3(kSThreads), smem, st, true, 1, a);
 }
 
 template <typename TQ, typename TP, int kCols>
@@ -669,8 +669,8 @@ cudaError_t launch_simt_cols(const AttnDev& a, int ctas, cudaStream_t st) {
   };
   cudaError_t e = allow_smem<k_attn_simt_tile<TQ, TP, kCols>>((int)bytes(32 * kCols));
   if (e != cudaSuccess) return e;
-  k_attn_simt_tile<TQ, TP, kCols><<<ctas, kSThreads, bytes(a.c.d), st>>>(a);
-  return cudaGetLastError();
+  return launch_ex(k_attn_simt_tile<TQ, TP, kCols>, dim3(ctas), dim3(kSThreads), bytes(a.c.d), st, true,
+                   1, a);
 }
 
 template <typename TQ, typename TP>

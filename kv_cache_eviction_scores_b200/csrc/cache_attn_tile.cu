@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(TileShared<TP, D, kAlt>::kThreads, 1) k_attn_t
   // with a quarter and three eighths of them there.)
   constexpr int kGoHalf = kScaled ? 1 : 0;
   extern __shared__ __align__(1024) uint8_t sm[];
-  pdl_trigger();
+  attn_begin();
   const uint32_t base = smem_u32(sm);
   if (base & 1023u) {  // the swizzled tiles need 1 KB alignment
     if (threadIdx.x == 0 && a.status) atomicMax(a.status, (int)DROPKV_ERR_CUDA);
@@ -820,8 +820,7 @@ cudaError_t launch_tile(const AttnDev& a, cudaStream_t st) {
   static_assert(smem <= 232448, "shared memory of a CTA");
   cudaError_t e = allow_smem<k_attn_tile<TP, D, kAlt>>(smem);
   if (e != cudaSuccess) return e;
-  kern<<<kTCtas, TileShared<TP, D, kAlt>::kThreads, smem, st>>>(a);
-  return cudaGetLastError();
+  return launch_ex(kern, dim3(kTCtas), dim3(TileShared<TP, D, kAlt>::kThreads), smem, st, true, 1, a);
 }
 
 template <bool kAlt>

@@ -274,3 +274,46 @@ def test_written_bits_over_all_magnitudes(src):
     assert torch.equal(ks.cpu().view(1, 1, n), byte) and torch.equal(vs, ks)
     assert torch.equal(kp.cpu().double().view(1, 1, n, d), want)
     assert torch.equal(vp.cpu().double().view(1, 1, n, d), -want)
+
+
+@pytest.mark.parametrize("T", [1, 3, 24, 90])
+def test_a_graph_that_reports_its_status(T):
+    s = make([200, 130], 8, 2, T, 128, 16, BF16, BF16, T)
+    lens = i32([200, 130])
+    want = dk.dropkv_cache_attention(s["q"], s["k"], s["v"], s["table"], lens)
+    out, status = torch.zeros_like(s["q"]), torch.full((1,), 9, dtype=torch.int32, device=DEV)
+    ws = torch.empty(96 << 20, dtype=torch.uint8, device=DEV)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        dk.dropkv_cache_attention(s["q"], s["k"], s["v"], s["table"], lens, out=out, workspace=ws,
+                                  status=status)
+    for length, code in ((200, dk.OK), (10 ** 6, dk.ERR_ARG), (200, dk.OK)):
+        lens[0] = length
+        g.replay()
+        torch.cuda.synchronize()
+        assert int(status) == code
+        if code == dk.OK:
+            assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("G,T", [(4, 1), (4, 4), (4, 20), (4, 60)])
+def test_calls_back_to_back_see_what_came_between(G, T):
+    # each call may be launched while its predecessor ends: lengths, queries and pages that a
+    # kernel between two calls changes are the second call's
+    s = make([900], G, 1, T, 128, 16, BF16, BF16, T)
+    lens = i32([300])
+    want = []
+    for L in (300, 301, 700):
+        lens.fill_(L)
+        torch.cuda.synchronize()
+        want.append(dk.dropkv_cache_attention(s["q"], s["k"], s["v"], s["table"], lens))
+        torch.cuda.synchronize()
+    for _ in range(20):
+        lens.fill_(300)
+        got = [dk.dropkv_cache_attention(s["q"], s["k"], s["v"], s["table"], lens)]
+        lens.add_(1)
+        got.append(dk.dropkv_cache_attention(s["q"], s["k"], s["v"], s["table"], lens))
+        lens.add_(399)
+        got.append(dk.dropkv_cache_attention(s["q"], s["k"], s["v"], s["table"], lens))
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
