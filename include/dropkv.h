@@ -345,7 +345,7 @@ DROPKV_API dropkv_status dropkv_cache_read(const dropkv_cache* cache,
  * has no influence on it, whatever it holds (NaN included).  Rows t >= n of out
  * and lse stay as they are.  Query head hq uses KV head hq / (Hq / Hkv).
  * Arithmetic: fp32; on the TENSOR path q, k and v enter as bf16 and the weights
- * that meet v are rounded to bf16.  *status_dev receives DROPKV_ERR_TIMEOUT if a
+ * that meet v as two bf16 parts (2^-15 of a weight off at most).  *status_dev receives DROPKV_ERR_TIMEOUT if a
  * wait inside a kernel gave up (its rows are then undefined). */
 typedef struct dropkv_cache_attn {
   const void* q;        /* device [B, Hq, T, d], strided (last index contiguous)    */

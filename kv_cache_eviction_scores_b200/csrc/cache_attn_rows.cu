@@ -6,11 +6,9 @@
 // units) and sum l: P = 2^(c q.k_j - m), l += sum P, O += P V; the reference
 // moves only when a logit exceeds it by more than 8 (2^8 fits every type
 // here), so O is rarely rescaled.  l sums the fp32 P; the P that meets V is
-// rounded to bf16 (nearest), which errs by at most 2^-8 of a weight, unbiased,
-// and together with the bf16 output's own rounding stays near sqrt(2) of the
-// latter alone.  e4m3 pages: a value is widened exactly to bf16, K's row scale
-// multiplies the logit and V's multiplies P before its rounding (a power of
-// two: exact), so nothing else is rounded.
+// taken as two bf16 parts (lower_bf16x2).  e4m3 pages: a value is widened exactly
+// to bf16, K's row scale multiplies the logit and V's multiplies P before it is
+// split (a power of two: exact), so nothing else is rounded.
 //
 // What bounds it: reading the pages.  Layout: a unit of 16 rows is one
 // m16n8k16 row block, so each K/V byte is used for 16 rows' products by the
@@ -361,8 +359,10 @@ __global__ void __launch_bounds__(kRThreads, 1) k_attn_rows(const AttnDev a) {
             }
           }
         }
-        const uint32_t pa[4] = {pack_bf16(p[0][0], p[0][1]), pack_bf16(p[0][2], p[0][3]),
-                                pack_bf16(p[1][0], p[1][1]), pack_bf16(p[1][2], p[1][3])};
+        const uint32_t pa[4] = {upper_bf16x2(p[0][0], p[0][1]), upper_bf16x2(p[0][2], p[0][3]),
+                                upper_bf16x2(p[1][0], p[1][1]), upper_bf16x2(p[1][2], p[1][3])};
+        const uint32_t pl[4] = {lower_bf16x2(p[0][0], p[0][1]), lower_bf16x2(p[0][2], p[0][3]),
+                                lower_bf16x2(p[1][0], p[1][1]), lower_bf16x2(p[1][2], p[1][3])};
         if (!kScaled && partly) {
           // A hidden slot's V may be an infinity or a NaN, and 0 * NaN must not
           // reach the rows that do not see it: such values are added to the rows
@@ -426,8 +426,12 @@ __global__ void __launch_bounds__(kRThreads, 1) k_attn_rows(const AttnDev a) {
             ldsm4t(r, tv + swz<kPieces>((mi & 1) * 8 + mr, c + (mi >> 1)));
 #pragma unroll
             for (int u = 0; u < 2; ++u) {  // even dims of the piece, then the odd ones
-              mma16816(o[2 * (c + u)], pa, widen2<kBytes02>(r[2 * u]), widen2<kBytes02>(r[2 * u + 1]));
-              mma16816(o[2 * (c + u) + 1], pa, widen2<kBytes13>(r[2 * u]), widen2<kBytes13>(r[2 * u + 1]));
+              const uint32_t e0 = widen2<kBytes02>(r[2 * u]), e1 = widen2<kBytes02>(r[2 * u + 1]);
+              const uint32_t d0 = widen2<kBytes13>(r[2 * u]), d1 = widen2<kBytes13>(r[2 * u + 1]);
+              mma16816(o[2 * (c + u)], pa, e0, e1);
+              mma16816(o[2 * (c + u) + 1], pa, d0, d1);
+              mma16816(o[2 * (c + u)], pl, e0, e1);
+              mma16816(o[2 * (c + u) + 1], pl, d0, d1);
             }
           }
         } else {
@@ -437,6 +441,8 @@ __global__ void __launch_bounds__(kRThreads, 1) k_attn_rows(const AttnDev a) {
             ldsm4t(r, tv + swz<kPieces>((mi & 1) * 8 + mr, c + (mi >> 1)));
             mma16816(o[c], pa, r[0], r[1]);
             mma16816(o[c + 1], pa, r[2], r[3]);
+            mma16816(o[c], pl, r[0], r[1]);
+            mma16816(o[c + 1], pl, r[2], r[3]);
           }
         }
       }
@@ -732,8 +738,10 @@ __global__ void __launch_bounds__(kRThreads, few_ctas_per_sm<TP>()) k_attn_few(c
           }
         }
         // P^T as a B fragment (k: slots, n: rows)
-        const uint32_t pb0 = transpose8(pack_bf16(p[0], p[1]));
-        const uint32_t pb1 = transpose8(pack_bf16(p[2], p[3]));
+        const uint32_t pb0 = transpose8(upper_bf16x2(p[0], p[1]));
+        const uint32_t pb1 = transpose8(upper_bf16x2(p[2], p[3]));
+        const uint32_t pl0 = transpose8(lower_bf16x2(p[0], p[1]));
+        const uint32_t pl1 = transpose8(lower_bf16x2(p[2], p[3]));
         if (!kScaled && partly) {
           // A hidden slot's V may be an infinity or a NaN, and 0 * NaN must not
           // reach the rows that do not see it: such values are added to the rows
@@ -789,6 +797,7 @@ __global__ void __launch_bounds__(kRThreads, few_ctas_per_sm<TP>()) k_attn_few(c
               const uint32_t va[4] = {widen2<kBytes02>(r[2 * u]), widen2<kBytes13>(r[2 * u]),
                                       widen2<kBytes02>(r[2 * u + 1]), widen2<kBytes13>(r[2 * u + 1])};
               mma16816(o[c + u], va, pb0, pb1);
+              mma16816(o[c + u], va, pl0, pl1);
             }
           }
         } else {
@@ -797,6 +806,7 @@ __global__ void __launch_bounds__(kRThreads, few_ctas_per_sm<TP>()) k_attn_few(c
             uint32_t r[4];  // dims 0-7 and 8-15 of slots 0-7, then of slots 8-15
             ldsm4t(r, tv + swz<kPieces>((mi >> 1) * 8 + mr, 2 * c + (mi & 1)));
             mma16816(o[c], r, pb0, pb1);
+            mma16816(o[c], r, pl0, pl1);
           }
         }
       }

@@ -4,7 +4,7 @@
 //
 // Mathematics: the online softmax of the row kernel (reference maximum in
 // log2 units that moves only when a logit exceeds it by more than 8; fp32 P
-// summed into l, P rounded to nearest bf16 for P V), one query row per thread.
+// summed into l, P as two bf16 parts for P V), one query row per thread.
 // e4m3 pages are widened to bf16 with their scale as they are staged: a
 // 4-bit significand times a power of two is a bf16 exactly, wherever bf16 has
 // the exponent (a row whose scale is under 2^-119 holds nothing above 2^-110,
@@ -15,9 +15,10 @@
 // warps there: page lookups, asynchronous 16-byte copies or, for e4m3, loads, the
 // widening and stores) is paid once per 256 rows.  Per query tile u: S_u = Q_u
 // K^T (M = N = 128) in TMEM columns 128 u, P_u over it (each half of P over the
-// half of S that it comes from), O_u at 256 + 128 u, all 512 columns.  One softmax warpgroup per query tile; while
-// one tile's softmax runs, the other tile's MMAs fill the tensor pipe.  P V of
-// a tile begins when the upper half of P is there.
+// half of S that it comes from; of each 16 slots eight columns of upper parts, then
+// eight of lower ones), O_u at 256 + 128 u, all 512 columns.  One softmax warpgroup
+// per query tile; while one tile's softmax runs, the other tile's MMAs fill the
+// tensor pipe.  P V of a tile begins when the upper half of P is there.
 // kAlt (units of at most 128 rows, which read more than they compute): one query
 // tile, one softmax warpgroup and eight producer warps; S of the next slot tile
 // goes to the other of two S/P buffers while this one's softmax runs, so that the
@@ -211,9 +212,9 @@ __global__ void __launch_bounds__(TileShared<TP, D, kAlt>::kThreads, 1) k_attn_t
   constexpr int kPieces = D / 8;  // of a staged row
   constexpr int kProd = S::kProd, kMine = 128 / kProd;  // producers, rows of a tile of each
   // The half of P whose end starts the second query tile.  Measured (512 tokens
-  // over 32K bf16 slots; 4 x 2048 over e4m3): no delay, upper half, lower half 331,
-  // 319, 309 and 791, 764, 808 us.  (Exponentials in part on the FMA pipe, by a
-  // polynomial, gained nothing once S was read less: 311 us without, 314 and 319
+  // over 32K bf16 slots; 4 x 2048 over e4m3): no delay, upper half, lower half 403,
+  // 398, 388 and 941, 898, 936 us.  (Exponentials in part on the FMA pipe, by a
+  // polynomial, gained nothing when P was one part: 311 us without, 314 and 319
   // with a quarter and three eighths of them there.)
   constexpr int kGoHalf = kScaled ? 1 : 0;
   extern __shared__ __align__(1024) uint8_t sm[];
@@ -281,8 +282,8 @@ __global__ void __launch_bounds__(TileShared<TP, D, kAlt>::kThreads, 1) k_attn_t
     // ---------------- MMA issuers ----------------
     // Warp u: S and P V of query tile u, so that no tile's products wait for the
     // other's softmax.  Measured against one warp for both, in turn or as they
-    // became ready: 331 against 350 and 377 us for 512 tokens over 32K bf16 slots
-    // (an MMA is issued as it executes, 64 clocks, and a barrier seen some 100
+    // became ready, when P was one part: 331 against 350 and 377 us for 512 tokens
+    // over 32K bf16 slots (an MMA is issued as it executes, 64 clocks, and a barrier seen some 100
     // clocks late).  kAlt: one warp, S a tile ahead of P V.
     const int u = warp - kTMmaWarp;
     constexpr uint32_t IDS = idesc_bf16(128, 128, false, false);  // S = Q K^T
@@ -346,8 +347,8 @@ __global__ void __launch_bounds__(TileShared<TP, D, kAlt>::kThreads, 1) k_attn_t
             tc_fence_after();
             if (lane == 0) {
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)  // V slices of 16 rows, 2 KB
-                mma_ts_w(dO, tbase + 128u * f + 64u * half + 8u * kk, vlo + 128u * (4 * half + kk),
+              for (int kk = 0; kk < 8; ++kk)  // both parts of P for each V slice of 16 rows, 2 KB
+                mma_ts_w(dO, tbase + 128u * f + 64u * half + 8u * kk, vlo + 128u * (4 * half + (kk >> 1)),
                          vd.hi, IDP, (j > 0 || half == 0 || kk > 0) ? 1u : 0u);
             }
           }
@@ -632,7 +633,7 @@ __global__ void __launch_bounds__(TileShared<TP, D, kAlt>::kThreads, 1) k_attn_t
     const uint32_t lane_off = (uint32_t)(ql * 32) << 16;
     const uint32_t tO = tbase + kTColO + 128u * u + lane_off;
     const float c = a.c_log2;
-    const uint64_t c2 = pk2(c, c);
+    const uint64_t c2 = pk2(c, c), above2 = pk2(kAboveOne, kAboveOne);
     uint32_t n = 0;              // slot tiles of this query tile so far
     uint32_t tiles = 0, units = 0;
     bool live = true;            // no wait has run out
@@ -719,16 +720,23 @@ __global__ void __launch_bounds__(TileShared<TP, D, kAlt>::kThreads, 1) k_attn_t
 #pragma unroll 1
           for (int half = 1; half >= 0; --half) {
             if (half == 0) tmem_ld64(tS, sr);  // the upper half is still there
-            uint32_t pw[32];
 #pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              float d0, d1;
-              upk2(ffma2(pk2(f32(sr[2 * k]), f32(sr[2 * k + 1])), c2, nmu2), d0, d1);
-              const float e0 = attn_ex2(d0), e1 = attn_ex2(d1);
-              l2 = fadd2(l2, pk2(e0, e1));
-              pw[k] = pack_bf16(e0, e1);
+            for (int z = 0; z < 4; ++z) {  // 16 slots at a time: there are no registers for more
+              uint32_t pw[16];  // the upper parts, the lower parts
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const int i = 16 * z + 2 * k;
+                float d0, d1;
+                upk2(ffma2(pk2(f32(sr[i]), f32(sr[i + 1])), c2, nmu2), d0, d1);
+                const float e0 = attn_ex2(d0), e1 = attn_ex2(d1);
+                const uint64_t e2 = pk2(e0, e1);
+                l2 = fadd2(l2, e2);
+                pw[k] = upper_bf16x2(e0, e1);
+                upk2(ffma2(e2, above2, pk2(minus_upper(e0), minus_upper(e1))), d0, d1);
+                pw[8 + k] = pack_bf16(d0, d1);
+              }
+              tmem_st16(tS + 64u * half + 16u * z, pw);
             }
-            tmem_st32(tS + 64u * half, pw);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();

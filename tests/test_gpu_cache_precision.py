@@ -1,0 +1,77 @@
+"""Cache attention's precision on the GPU against fp64: the weights that meet V."""
+
+import math
+
+import pytest
+import torch
+
+import cache_ref as R
+import kv_cache_eviction_scores_b200 as dk
+from cache_ref import BF16, E4M3
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def line(L, Hkv, d, dtype, gen, byte=121):
+    """One sequence's pages of 64 slots: (pages, scale, table, dense fp64 [Hkv, L, d])."""
+    n = -(-L // 64)
+    x = torch.randn(n, Hkv, 64, d, generator=gen, device=DEV)
+    x = (x * 48).to(E4M3) if dtype == E4M3 else x.to(dtype)
+    scale = torch.full((n, Hkv, 64), byte, dtype=torch.uint8, device=DEV) if dtype == E4M3 else None
+    dense = x.double() * (1.0 if scale is None else 2.0 ** (byte - 127))
+    return x, scale, dense.permute(1, 0, 2, 3).reshape(Hkv, n * 64, d)[:, :L]
+
+
+# rows per KV head of each of the tensor path's kernels
+@pytest.mark.parametrize("pt", [BF16, E4M3])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G,T", [(4, 1), (4, 4), (4, 20), (4, 100)])
+def test_the_weights_that_meet_v_keep_fifteen_bits(pt, d, G, T):
+    # Two bf16 parts of a weight leave 2^-15 of it (the lower part, at most 2^-7 of the weight, is
+    # rounded by 2^-8 of itself at most), and the factor 1 + 2^-20 that keeps the lower part above
+    # zero adds its own.  Everything else is R.bounds' fp32 arithmetic and the output's rounding.
+    # One bf16 part would be off by 2^-8 of a weight, which shows wherever V's values cancel.
+    g = torch.Generator(device=DEV).manual_seed(G * T + d)
+    Hkv, L = 2, T + 100
+    k, ks, K = line(L, Hkv, d, pt, g)
+    v, vs, V = line(L, Hkv, d, pt, g)
+    q = torch.randn(1, G * Hkv, T, d, generator=g, device=DEV).to(BF16)
+    table = torch.arange(k.shape[0], dtype=torch.int32, device=DEV)[None]
+    out, lse = dk.dropkv_cache_attention(q, k, v, table, i32([L]), k_scale=ks, v_scale=vs,
+                                         return_lse=True, sync=True)
+    x = q[0].double().view(Hkv, G, T, d)
+    y = torch.einsum("hgtd,hjd->hgtj", x, K) / math.sqrt(d)
+    seen = torch.arange(L, device=DEV) <= (L - T + torch.arange(T, device=DEV))[:, None]
+    p = y.masked_fill(~seen, -math.inf).softmax(-1)
+    o, A = torch.einsum("hgtj,hjd->hgtd", p, V), torch.einsum("hgtj,hjd->hgtd", p, V.abs())
+    S = (torch.einsum("hgtd,hjd->hgtj", x.abs(), K.abs()) / math.sqrt(d)).masked_fill(~seen, 0).amax(-1)
+    Y = y.abs().masked_fill(~seen, 0).amax(-1)
+    lw = torch.logsumexp(y.masked_fill(~seen, -math.inf), -1)
+    tol, _ = R.bounds(o, lw, A, S, Y, d, L, BF16, False)
+    tol = tol + A * (2.0 ** -15 + 2.0 ** -20)
+    err = (out[0].double().view(Hkv, G, T, d) - o).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G,T", [(4, 1), (4, 4), (4, 20), (4, 100)])
+def test_infinities_that_a_row_sees_reach_it(d, G, T):
+    # equal weights of a power of two: their lower parts would be 0, and 0 * inf is NaN
+    g = torch.Generator(device=DEV).manual_seed(G * T + d)
+    Hkv, L = 2, T + 300
+    k, _, _ = line(L, Hkv, d, BF16, g)
+    v, _, V = line(L, Hkv, d, BF16, g)
+    k.zero_()
+    v[0, :, 9, 3], v[1, :, 4, 5], v[0, :, 20, d - 1] = math.inf, -math.inf, math.nan
+    q = torch.randn(1, G * Hkv, T, d, generator=g, device=DEV).to(BF16)
+    table = torch.arange(k.shape[0], dtype=torch.int32, device=DEV)[None]
+    out = dk.dropkv_cache_attention(q, k, v, table, i32([L]), sync=True)[0]
+    assert (out[..., 3] == math.inf).all() and (out[..., 5] == -math.inf).all()
+    assert torch.isnan(out[..., d - 1]).all()
+    rest = [i for i in range(d) if i not in (3, 5, d - 1)]
+    assert torch.isfinite(out[..., rest]).all()
