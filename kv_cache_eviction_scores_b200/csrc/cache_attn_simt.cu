@@ -223,15 +223,20 @@ __global__ void __launch_bounds__(kSThreads, 4) k_attn_simt(const AttnDev a) {
             const int col = lane + 32 * i;
             if (32 * i >= d) break;
             const float* v = sV + (col < d ? col : 0);
+            // the tile's slots by themselves: a chain over all of a long cache's slots
+            // loses bits (7e-4 of a sum of 64K equal terms)
+            float y[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
             for (int j = 0; j < kSTile; ++j) {
               const float4 p4 = four(sP + j * 4);
               const float x = v[j * ds];
-              o[0][i] = fmaf(p4.x, x, o[0][i]);
-              o[1][i] = fmaf(p4.y, x, o[1][i]);
-              o[2][i] = fmaf(p4.z, x, o[2][i]);
-              o[3][i] = fmaf(p4.w, x, o[3][i]);
+              y[0] = fmaf(p4.x, x, y[0]);
+              y[1] = fmaf(p4.y, x, y[1]);
+              y[2] = fmaf(p4.z, x, y[2]);
+              y[3] = fmaf(p4.w, x, y[3]);
             }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[k][i] += y[k];
           }
         } else {
           // a slot that a row does not see may hold anything: 0 * NaN must not
@@ -423,27 +428,46 @@ __global__ void __launch_bounds__(kSThreads, kCols > 4 ? 1 : kCols > 2 ? 2 : 3) 
         }
         __syncwarp();
         if (!partly) {
+          // the tile's slots by themselves, as in the kernel above; 128 columns at a
+          // time, so that the sums fit the registers (d = 256 then reads P twice: 505 us
+          // against 451 for 300 rows x 8 over 3000 fp32 slots; d = 128 199 and 201)
+          constexpr int kPart = kCols < 4 ? kCols : 4;
+#pragma unroll
+          for (int i0 = 0; i0 < kCols; i0 += kPart) {
+            uint64_t y[4][kPart][2];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int i = 0; i < kPart; ++i) y[k][i][0] = y[k][i][1] = 0ull;
 #pragma unroll 1
-          for (int j = 0; j < kSTile; j += 4) {
-            float4 p[4];
+            for (int j = 0; j < kSTile; j += 4) {
+              float4 p[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) p[k] = four(sP + (4 * ty + k) * kPStride + j);
+              for (int k = 0; k < 4; ++k) p[k] = four(sP + (4 * ty + k) * kPStride + j);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float* v = sV + (j + e) * ds;
+              for (int e = 0; e < 4; ++e) {
+                const float* v = sV + (j + e) * ds;
 #pragma unroll
-              for (int i = 0; i < kCols; ++i) {
-                const float4 x = four(v + min(4 * tx + 32 * i, d4 - 4));
-                const uint64_t xa = lo2(x), xb = hi2(x);
+                for (int i = 0; i < kPart; ++i) {
+                  const float4 x = four(v + min(4 * tx + 32 * (i0 + i), d4 - 4));
+                  const uint64_t xa = lo2(x), xb = hi2(x);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const float pe = e == 0 ? p[k].x : e == 1 ? p[k].y : e == 2 ? p[k].z : p[k].w;
-                  const uint64_t p2 = tc::pk2(pe, pe);
-                  o[k][i][0] = tc::ffma2(p2, xa, o[k][i][0]);
-                  o[k][i][1] = tc::ffma2(p2, xb, o[k][i][1]);
+                  for (int k = 0; k < 4; ++k) {
+                    const float pe = e == 0 ? p[k].x : e == 1 ? p[k].y : e == 2 ? p[k].z : p[k].w;
+                    const uint64_t p2 = tc::pk2(pe, pe);
+                    y[k][i][0] = tc::ffma2(p2, xa, y[k][i][0]);
+                    y[k][i][1] = tc::ffma2(p2, xb, y[k][i][1]);
+                  }
                 }
               }
             }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int i = 0; i < kPart; ++i) {
+                o[k][i0 + i][0] = tc::fadd2(o[k][i0 + i][0], y[k][i][0]);
+                o[k][i0 + i][1] = tc::fadd2(o[k][i0 + i][1], y[k][i][1]);
+              }
           }
         } else {
           // a slot that a row does not see may hold anything: 0 * NaN must not

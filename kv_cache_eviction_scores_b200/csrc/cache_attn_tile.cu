@@ -716,7 +716,7 @@ __global__ void __launch_bounds__(TileShared<TP, D, kAlt>::kThreads, 1) k_attn_t
           }
           const float mu = m == -CUDART_INF_F ? 0.f : m;
           const uint64_t nmu2 = pk2(-mu, -mu);
-          uint64_t l2 = pk2(l, 0.f);
+          uint64_t l2 = 0ull;  // of this tile: a chain over all slots would lose bits
 #pragma unroll 1
           for (int half = 1; half >= 0; --half) {
             if (half == 0) tmem_ld64(tS, sr);  // the upper half is still there
@@ -745,7 +745,7 @@ __global__ void __launch_bounds__(TileShared<TP, D, kAlt>::kThreads, 1) k_attn_t
           }
           float la, lb;
           upk2(l2, la, lb);
-          l = la + lb;
+          l += la + lb;
         } else {
           tc_fence_before();
           __syncwarp();

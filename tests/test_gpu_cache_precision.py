@@ -1,4 +1,5 @@
-"""Cache attention's precision on the GPU against fp64: the weights that meet V."""
+"""Cache attention's precision on the GPU against fp64: the weights that meet V, and
+sums over long ranges of slots."""
 
 import math
 
@@ -7,7 +8,7 @@ import torch
 
 import cache_ref as R
 import kv_cache_eviction_scores_b200 as dk
-from cache_ref import BF16, E4M3
+from cache_ref import BF16, E4M3, F32
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -75,3 +76,37 @@ def test_infinities_that_a_row_sees_reach_it(d, G, T):
     assert torch.isnan(out[..., d - 1]).all()
     rest = [i for i in range(d) if i not in (3, 5, d - 1)]
     assert torch.isfinite(out[..., rest]).all()
+
+
+@pytest.mark.parametrize("pt", [BF16, E4M3, F32])
+@pytest.mark.parametrize("rows", [(1, 128), (1, 512)])
+@pytest.mark.parametrize("c", [0.34375, 0.5625, 0.625])
+def test_sums_over_a_long_range_that_no_split_shortens(pt, rows, c):
+    # The first 128 slots' logits are c and set the reference; all others are 0, so that every
+    # weight behind them is exp(-c) and the sums' roundings all go one way.  With units to fill
+    # the CTAs, one CTA sums all slots of a row.  A tile's slots (128 on the tensor path, 32 on
+    # CUDA cores) are summed by themselves, in at most 128 additions of 2^-24 each, and then added
+    # to the total: n / 128 or n / 32 additions more.  The weights' own errors are ex2's 2^-22 and
+    # the exponent's rounding, 2^-24 of c.
+    G, T = rows
+    d, Hkv = 64, 8
+    L, B, tile = (65536, 12, 32) if pt == F32 else (131072, 20, 128)
+    n = L // 64
+    k = torch.zeros(n, Hkv, 64, d, device=DEV)
+    k[:2, :, :, 0] = c
+    k = k.to(pt)
+    v = torch.full_like(k.float(), 3.0).to(pt)
+    sc = torch.full((n, Hkv, 64), 127, dtype=torch.uint8, device=DEV) if pt == E4M3 else None
+    # one set of pages for all sequences
+    table = torch.arange(n, dtype=torch.int32, device=DEV)[None].repeat(B, 1)
+    q = torch.zeros(B, Hkv * G, T, d, dtype=F32 if pt == F32 else BF16, device=DEV)
+    q[..., 0] = 8.0                                  # times the default scale of 1 / 8
+    out, lse = dk.dropkv_cache_attention(q, k, v, table, i32([L] * B), causal=False, k_scale=sc,
+                                         v_scale=sc, return_lse=True, sync=True)
+    rel = (128 + L / tile) * 2.0 ** -24 + 2.0 ** -21
+    want = math.log(128 * math.exp(c) + L - 128)
+    err = float((lse.double() - want).abs().max())
+    assert err <= rel + want * 2.0 ** -22, err
+    tol = 3.0 * (2 * rel + 2.0 ** -22 + (2.0 ** -8 if pt != F32 else 0.0))
+    err = float((out.double() - 3.0).abs().max())
+    assert err <= tol, err
