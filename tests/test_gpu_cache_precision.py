@@ -9,6 +9,7 @@ import torch
 import cache_ref as R
 import kv_cache_eviction_scores_b200 as dk
 from cache_ref import BF16, E4M3, F32
+from test_gpu_cache_tiles import dense, make
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -110,3 +111,33 @@ def test_sums_over_a_long_range_that_no_split_shortens(pt, rows, c):
     tol = 3.0 * (2 * rel + 2.0 ** -22 + (2.0 ** -8 if pt != F32 else 0.0))
     err = float((out.double() - 3.0).abs().max())
     assert err <= tol, err
+
+
+@pytest.mark.parametrize("G,T", [(4, 1), (4, 4), (4, 30), (4, 80)])
+@pytest.mark.parametrize("path", ["auto", "simt"])
+def test_small_scales_of_v_keep_their_precision(G, T, path):
+    # V's scales are 2^-115 to 2^-98, so outputs are some 2^-100.  Tensor path: a weight times such a
+    # scale can lie among bf16's subnormals, whose step of 2^-133 its two parts resolve to 2^-134;
+    # with V's own values (at most 448) over n slots, and a sum of weights of at least 1 (the
+    # reference is some slot's logit): 448 n 2^-134.  CUDA cores: V times its scale is exact in fp32.
+    # Nothing else depends on the scale.
+    lengths, n = [300, 171], [T, max(1, T - 2)]
+    s = make(lengths, 2 * G, 2, T, 128, 16, BF16, E4M3, T, (118, 123), (12, 30))
+    out = dk.dropkv_cache_attention(s["q"], s["k"], s["v"], s["table"], i32(lengths),
+                                    q_lengths=i32(n), k_scale=s["ks"], v_scale=s["vs"], path=path,
+                                    sync=True)
+    for b, (L, c) in enumerate(zip(lengths, n)):
+        K, V = (dense(s[x], s[x + "s"], s["table"][b], L) for x in "kv")
+        x = s["q"][b, :, :c].double().view(2, G, c, 128)
+        y = torch.einsum("hgtd,hjd->hgtj", x, K) / math.sqrt(128)
+        seen = torch.arange(L, device=DEV) <= (L - c + torch.arange(c, device=DEV))[:, None]
+        w = torch.logsumexp(y.masked_fill(~seen, -math.inf), -1)
+        p = torch.exp(y.masked_fill(~seen, -math.inf) - w[..., None])
+        o, A = torch.einsum("hgtj,hjd->hgtd", p, V), torch.einsum("hgtj,hjd->hgtd", p, V.abs())
+        S = torch.einsum("hgtd,hjd->hgtj", x.abs(), K.abs()) / math.sqrt(128)
+        S, Y = S.masked_fill(~seen, 0).amax(-1), y.abs().masked_fill(~seen, 0).amax(-1)
+        tol = R.bounds(o, w, A, S, Y, 128, L, BF16, False)[0] - 1e-30
+        if path == "auto":
+            tol = tol + A * (2.0 ** -15 + 2.0 ** -20) + 448 * L * 2.0 ** -134
+        err = (out[b, :, :c].double().view(2, G, c, 128) - o).abs()
+        assert bool((err <= tol).all()), float((err / tol).max())
