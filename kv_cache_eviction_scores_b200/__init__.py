@@ -770,8 +770,13 @@ def evict_to_cache(q, k, v, window: int, pool_kernel: int, keep_counts: Sequence
                    score: str = "perturbation"):
     """Scores the prompt's tokens, lists the kept ones, and writes their K/V rows
     into slots 0.. of a paged cache: (cache lengths int32 [B], scores, keep_idx,
-    evict_idx).  The arguments are evict's and dropkv_cache_write's."""
-    _cache(k_pages, v_pages, page_table, k_scale, v_scale)  # refuse before any work
+    evict_idx).  The arguments are evict's and dropkv_cache_write's, and refused
+    before any work."""
+    _cache(k_pages, v_pages, page_table, k_scale, v_scale)
+    dev, (_, Hkv, _, d) = k_pages.device, k_pages.shape
+    _check_inputs(q, k, v)
+    shape = (page_table.shape[0], Hkv, k.shape[2] if k.dim() == 4 else 0, d)
+    _dense(k, "k", dev, shape), _dense(v, "v", dev, shape)
     keep = [int(x) for x in keep_counts]
     if keep and max(keep) > page_table.shape[1] * k_pages.shape[2]:
         raise ValueError("the page table has too few pages for the kept tokens")
