@@ -357,7 +357,7 @@ typedef struct dropkv_cache_attn {
   int32_t Hq;           /* a multiple of the cache's Hkv                            */
   int32_t T;            /* >= 1                                                     */
   int32_t causal;       /* 0 or 1                                                   */
-  float scale;          /* > 0, or 0 for 1/sqrt(d)                                  */
+  float scale;          /* > 0, up to FLT_MAX / log2(e); or 0 for 1/sqrt(d)         */
   int32_t path;         /* dropkv_path: AUTO, SIMT (fp32 CUDA cores, any shape) or
                            TENSOR (bf16 q; bf16 or E4M3 pages; d 64 or 128; q, out
                            and their strides multiples of 16 bytes)                 */

@@ -711,6 +711,9 @@ def dropkv_cache_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torc
     with ``return_lse`` or when given.  ``path``: "auto", "simt" (fp32 CUDA
     cores) or "tensor".  The other arguments are dropkv_cache_write's.
     """
+    # in fp32, where a small one would become the library's 0 for the default
+    if scale is not None and not 0.0 < ctypes.c_float(scale).value < float("inf"):
+        raise ValueError("scale must be positive and finite in fp32")
     c = _cache(k_pages, v_pages, page_table, k_scale, v_scale)
     dev = k_pages.device
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
@@ -735,8 +738,6 @@ def dropkv_cache_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torc
         return_lse = True
     elif return_lse:
         lse = torch.zeros(B, Hq, T, device=dev)
-    if scale is not None and not (0.0 < scale < float("inf")):
-        raise ValueError("scale must be positive and finite")
     if lengths is None:
         raise ValueError("lengths are needed")
     a = _ATTN_BYTES(q.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(), *qs, *os_,

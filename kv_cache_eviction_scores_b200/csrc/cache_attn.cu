@@ -1,5 +1,6 @@
 // cache_attn.cu -- dropkv_cache_attention's entry points: argument checks, the
 // choice of the path, the workspace and the launches.
+#include <float.h>
 #include <math.h>
 
 #include <algorithm>
@@ -10,6 +11,8 @@ namespace dropkv {
 
 namespace {
 
+constexpr double kLog2E = 1.4426950408889634;
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 dropkv_status check_attn(const dropkv_cache* c, const dropkv_cache_attn* t, bool pointers) {
@@ -18,7 +21,7 @@ dropkv_status check_attn(const dropkv_cache* c, const dropkv_cache_attn* t, bool
   if (!t || t->Hq < 1 || t->Hq % c->Hkv != 0 || t->T < 1) return DROPKV_ERR_ARG;
   if (t->dtype != DROPKV_BF16 && t->dtype != DROPKV_F32) return DROPKV_ERR_ARG;
   if (t->causal != 0 && t->causal != 1) return DROPKV_ERR_ARG;
-  if (!(t->scale >= 0.f) || isinf(t->scale)) return DROPKV_ERR_ARG;
+  if (!(t->scale >= 0.f) || t->scale * kLog2E > FLT_MAX) return DROPKV_ERR_ARG;
   if (t->path != DROPKV_PATH_AUTO && t->path != DROPKV_PATH_SIMT && t->path != DROPKV_PATH_TENSOR)
     return DROPKV_ERR_ARG;
   // rows of a group and (sequence, row tile) items are 32-bit
@@ -141,7 +144,7 @@ extern "C" dropkv_status dropkv_cache_attention(const dropkv_cache* cache,
   a.fG = FastDiv::of((uint32_t)a.G);
   a.nrt = (a.G * t.T + g.rows - 1) / g.rows;
   const double scale = t.scale > 0.f ? (double)t.scale : 1.0 / sqrt((double)c.d);
-  a.c_log2 = (float)(scale * 1.4426950408889634);
+  a.c_log2 = (float)(scale * kLog2E);
   a.lengths = t.lengths;
   a.q_lengths = t.q_lengths;
   a.part = reinterpret_cast<float*>(workspace);
