@@ -313,8 +313,8 @@ typedef struct dropkv_cache_rows {
   int64_t v_stride[3];
   int32_t dtype;        /* DROPKV_BF16 or DROPKV_F32                                */
   int32_t n;            /* rows of the dense tensors per (sequence, head)           */
-  int32_t m;            /* rows moved at most per (sequence, head), >= 1; without a
-                           list, and on a read, m <= n                              */
+  int32_t m;            /* rows moved at most per (sequence, head), 1..0x7fff0000;
+                           without a list, and on a read, m <= n                    */
   int32_t reserved;     /* 0                                                        */
   const int32_t* rows;  /* device int32 [B, Hkv, m] or NULL: the list (a keep_idx of
                            dropkv_select is one); an entry of -1 is skipped         */

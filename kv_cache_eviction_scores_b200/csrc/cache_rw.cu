@@ -359,6 +359,8 @@ dropkv_status run_rows(const dropkv_cache* cp, const dropkv_cache_rows* rp, int3
   if (!r.k || !r.v || r.n < 1 || r.m < 1 || r.reserved != 0) return DROPKV_ERR_ARG;
   if (r.dtype != DROPKV_BF16 && r.dtype != DROPKV_F32) return DROPKV_ERR_ARG;
   if ((!r.rows || !kWrite) && r.m > r.n) return DROPKV_ERR_ARG;
+  // the kernel counts a block's items in 32 bits past the last one (slots end there, too)
+  if (r.m > 0x7FFF0000) return DROPKV_ERR_ARG;
   const int esz = r.dtype == DROPKV_BF16 ? 2 : 4;
   if (((uintptr_t)r.k | (uintptr_t)r.v) % esz) return DROPKV_ERR_ARG;
   if (((uintptr_t)r.rows | (uintptr_t)r.start | (uintptr_t)r.counts | (uintptr_t)status_dev) & 3u)

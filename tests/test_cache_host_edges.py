@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import kv_cache_eviction_scores_b200 as dk
-from test_cache_host import _attend, _attn, _cache
+from test_cache_host import FAKE, _attend, _attn, _cache, _call, _rows
 
 
 @pytest.mark.parametrize("scale", [1e-46, 1e39, 0.0, -1.0, float("nan"), float("inf")])
@@ -22,3 +22,14 @@ def test_a_scale_that_overflows_in_units_of_log2_is_refused():
     if not torch.cuda.is_available():
         for fine in (2.3e38, 1e-45):
             assert _attend(_cache(), _attn(scale=fine)) == dk.ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("name", ["dropkv_cache_write", "dropkv_cache_read"])
+@pytest.mark.parametrize("listed", [None, FAKE])
+def test_more_rows_than_the_kernel_counts_are_refused(name, listed):
+    # a block's items past the last one would pass 2^31 and be looked up in front of the list
+    fn, top = getattr(dk.lib(), name), 2 ** 31 - 1
+    for m in (top, 0x7FFF0001):
+        assert _call(fn, _cache(), _rows(n=top, m=m, rows=listed)) == dk.ERR_ARG
+    if not torch.cuda.is_available():
+        assert _call(fn, _cache(), _rows(n=top, m=0x7FFF0000, rows=listed)) == dk.ERR_UNSUPPORTED
