@@ -431,6 +431,17 @@ DROPKV_API dropkv_status dropkv_selftest_select_timeout(int32_t B, int32_t Hkv, 
                                                         int32_t* status_dev, uint64_t limit_ns,
                                                         void* stream);
 
+/* Self-test of the failure path of dropkv_cache_attention's waits (those of its
+ * tcgen05 kernel, which takes the TENSOR path's calls of more than 16 query rows
+ * per KV head; other calls give DROPKV_ERR_UNSUPPORTED): runs the call with one
+ * warp of every CTA withholding the first hand-over of its queries and every wait
+ * limited to about limit_ns nanoseconds (0 < limit_ns <= 1e9).  *status_dev (not
+ * NULL) ends as DROPKV_ERR_TIMEOUT and out and lse are undefined.  Asynchronous; no
+ * fault or trap is involved and the context stays usable. */
+DROPKV_API dropkv_status dropkv_selftest_cache_attention_timeout(
+    const dropkv_cache* cache, const dropkv_cache_attn* attn, void* workspace,
+    size_t workspace_bytes, int32_t* status_dev, uint64_t limit_ns, void* stream);
+
 /* DROPKV_ABI_VERSION of the loaded library. */
 DROPKV_API int32_t dropkv_abi_version(void);
 

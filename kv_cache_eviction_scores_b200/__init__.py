@@ -51,7 +51,7 @@ __all__ = [
     "dropkv_select", "evict", "evict_to_cache", "dropkv_cache_write", "dropkv_cache_read",
     "dropkv_cache_attention", "cache_attention_workspace_bytes", "cache_attention_path",
     "Cache", "CacheRows", "CacheAttn", "auto_path", "scores_launches", "select_launches",
-    "selftest_wait_timeout", "selftest_select_timeout",
+    "selftest_wait_timeout", "selftest_select_timeout", "selftest_cache_attention_timeout",
     "OK", "ERR_ARG", "ERR_SINGULAR", "ERR_CUDA", "ERR_UNSUPPORTED", "ERR_WORKSPACE", "ERR_TIMEOUT",
     "PATH_AUTO", "PATH_SIMT", "PATH_TENSOR", "SCORE_PERTURBATION", "SCORE_ATTENTION",
 ]
@@ -183,6 +183,8 @@ def lib():
     L.dropkv_cache_attention.restype = i32
     L.dropkv_cache_attention_path.argtypes = [cp, ap]
     L.dropkv_cache_attention_path.restype = i32
+    L.dropkv_selftest_cache_attention_timeout.argtypes = [cp, ap, vp, sz, vp, ctypes.c_uint64, vp]
+    L.dropkv_selftest_cache_attention_timeout.restype = i32
     _lib = L
     return L
 
@@ -761,6 +763,38 @@ def dropkv_cache_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torc
         workspace, size = torch.empty(need, dtype=torch.uint8, device=dev), need
     _launch(attend, "dropkv_cache_attention", (c, a, workspace.data_ptr(), size), dev, status, sync)
     return (out, lse) if return_lse else out
+
+
+def selftest_cache_attention_timeout(T: int = 40, e4m3: bool = False, d: int = 128, B: int = 2,
+                                     limit_ms: float = 20.0, device=None) -> int:
+    """Runs dropkv_cache_attention's tcgen05 kernel over a small cache (B sequences
+    of some 400 slots, two query heads on one KV head, T > 8 new tokens) with one
+    hand-over of every CTA withheld and its waits limited to ``limit_ms``; returns the
+    status word: ERR_TIMEOUT when they gave up as designed."""
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else \
+        torch.device(device)
+    pages = 16  # the sequences share them
+    table = torch.arange(pages, dtype=torch.int32, device=dev).repeat(B, 1)
+    q = torch.zeros(B, 2, T, d, dtype=torch.bfloat16, device=dev)
+    out = torch.empty_like(q)
+    lengths = torch.tensor([400 + b % 12 for b in range(B)], dtype=torch.int32, device=dev)
+    kv = torch.zeros(pages, 1, 32, d, dtype=torch.uint8 if e4m3 else torch.bfloat16, device=dev)
+    scale = torch.zeros(pages, 1, 32, dtype=torch.uint8, device=dev)
+    strides = (ctypes.c_int64 * 3)(*q.stride()[:3])
+    c = Cache(B, 1, d, pages, 32, pages, E4M3 if e4m3 else BF16, 0, kv.data_ptr(), kv.data_ptr(),
+              scale.data_ptr() if e4m3 else None, scale.data_ptr() if e4m3 else None,
+              table.data_ptr())
+    a = CacheAttn(q.data_ptr(), out.data_ptr(), None, strides, strides, BF16, 2, T, 1, 0.0,
+                  PATH_TENSOR, lengths.data_ptr(), None)
+    size = cache_attention_workspace_bytes(c, a)
+    ws = torch.empty(max(size, 16), dtype=torch.uint8, device=dev)
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    with torch.cuda.device(dev):
+        _check(lib().dropkv_selftest_cache_attention_timeout(
+            ctypes.byref(c), ctypes.byref(a), _ptr(ws), size, _ptr(status), int(limit_ms * 1e6),
+            _stream(dev)), "dropkv_selftest_cache_attention_timeout")
+    torch.cuda.synchronize(dev)
+    return int(status.item())
 
 
 def evict_to_cache(q, k, v, window: int, pool_kernel: int, keep_counts: Sequence[int],

@@ -104,11 +104,10 @@ extern "C" int32_t dropkv_cache_attention_path(const dropkv_cache* cache,
   return path_of(*cache, *attn);
 }
 
-extern "C" dropkv_status dropkv_cache_attention(const dropkv_cache* cache,
-                                                const dropkv_cache_attn* attn, void* workspace,
-                                                size_t workspace_bytes, int32_t* status_dev,
-                                                void* stream) {
-  NvtxRange range("dropkv_cache_attention");
+// The call; `limit_ns` > 0: the tile kernel's self-test, with a wait that runs out.
+static dropkv_status run_attention(const dropkv_cache* cache, const dropkv_cache_attn* attn,
+                                   void* workspace, size_t workspace_bytes, int32_t* status_dev,
+                                   uint64_t limit_ns, void* stream) {
   dropkv_status s = check_attn(cache, attn, true);
   if (s != DROPKV_OK) return s;
   const dropkv_cache& c = *cache;
@@ -116,6 +115,10 @@ extern "C" dropkv_status dropkv_cache_attention(const dropkv_cache* cache,
   if ((uintptr_t)status_dev & 3u) return DROPKV_ERR_ARG;
   const int path = path_of(c, t);
   if (path < 0) return DROPKV_ERR_UNSUPPORTED;
+  const bool tensor = path == DROPKV_PATH_TENSOR;
+  const Tensor kind = tensor_of(c, t);
+  if (limit_ns > 0 && (!tensor || kind == Tensor::kFew || kind == Tensor::kRows))
+    return DROPKV_ERR_UNSUPPORTED;  // no waits to run out
   if (!workspace || !aligned16(workspace) ||
       workspace_bytes < dropkv_cache_attention_workspace_bytes(cache, attn))
     return DROPKV_ERR_WORKSPACE;
@@ -125,8 +128,6 @@ extern "C" dropkv_status dropkv_cache_attention(const dropkv_cache* cache,
   if (status_dev)
     if (cudaError_t e = cudaMemsetAsync(status_dev, 0, sizeof(int32_t), st)) return cuda_fail(e);
 
-  const bool tensor = path == DROPKV_PATH_TENSOR;
-  const Tensor kind = tensor_of(c, t);
   const AttnGrid g = tensor ? grid_of(kind, c.dtype) : attn_grid_simt(group_rows(c, t), c.d);
   AttnDev a = {};
   a.c = cache_dev(c);
@@ -150,6 +151,9 @@ extern "C" dropkv_status dropkv_cache_attention(const dropkv_cache* cache,
   a.part = reinterpret_cast<float*>(workspace);
   a.pstride = (c.d + 3) / 4 * 4 + 4;
   a.status = status_dev;
+  a.withhold = limit_ns > 0;
+  // the SM clock stays below 2 GHz
+  a.wait_clocks = limit_ns > 0 ? 2 * (long long)limit_ns : kWaitClocks;
   cudaError_t e;
   if (!tensor)
     e = launch_attn_simt(a, g, c.dtype, t.dtype, st);
@@ -161,4 +165,19 @@ extern "C" dropkv_status dropkv_cache_attention(const dropkv_cache* cache,
     e = launch_attn_tile(a, c.dtype, kind == Tensor::kTile128, st);
   if (e == cudaSuccess) e = launch_attn_merge(a, g, t.dtype, st);
   return e == cudaSuccess ? DROPKV_OK : cuda_fail(e);
+}
+
+extern "C" dropkv_status dropkv_cache_attention(const dropkv_cache* cache,
+                                                const dropkv_cache_attn* attn, void* workspace,
+                                                size_t workspace_bytes, int32_t* status_dev,
+                                                void* stream) {
+  NvtxRange range("dropkv_cache_attention");
+  return run_attention(cache, attn, workspace, workspace_bytes, status_dev, 0, stream);
+}
+
+extern "C" dropkv_status dropkv_selftest_cache_attention_timeout(
+    const dropkv_cache* cache, const dropkv_cache_attn* attn, void* workspace,
+    size_t workspace_bytes, int32_t* status_dev, uint64_t limit_ns, void* stream) {
+  if (!status_dev || limit_ns == 0 || limit_ns > 1000000000ull) return DROPKV_ERR_ARG;
+  return run_attention(cache, attn, workspace, workspace_bytes, status_dev, limit_ns, stream);
 }

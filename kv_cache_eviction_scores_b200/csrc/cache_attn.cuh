@@ -32,7 +32,11 @@ struct AttnDev {
   float* part;      // [2 grid][rows][pstride]
   int32_t pstride;  // floats of a partial row: O (d rounded up to 4), m, l, pad
   int32_t* status;
+  long long wait_clocks;  // limit of every wait on an mbarrier
+  int32_t withhold;       // 1 in the self-test alone: the first unit's queries are never handed over
 };
+// Of a wait: two seconds at least.
+constexpr long long kWaitClocks = 4000000000ll;
 
 // An attention kernel's first step.  It may be launched while its predecessor in
 // the stream ends, and waits for that here; only then may the join be launched,

@@ -31,7 +31,7 @@
 // 0 * NaN must not reach the other rows: the producers stage such values as 0
 // and raise the unit's flag, and the rows that do see them add them at the end.
 //
-// Every wait on an mbarrier is bounded (some two seconds); on expiry the
+// Every wait on an mbarrier is bounded (kWaitClocks, or the self-test's limit); on expiry the
 // kernel records DROPKV_ERR_TIMEOUT, every role leaves, and TMEM is freed.
 #include <type_traits>
 
@@ -46,7 +46,6 @@ using namespace tc;
 
 constexpr int kTTile = 128, kTCtas = 148;
 constexpr int kTMmaWarp = 12;  // the softmax warps, the producers, then the MMA issuers
-constexpr long long kTWaitClocks = 4000000000ll;  // of a wait: two seconds at least
 constexpr uint32_t kTColO = 256;
 
 
@@ -81,16 +80,12 @@ __device__ __forceinline__ void fail(const AttnDev& a) {
 }
 // Waits are bounded by the SM's clock: reading %globaltimer takes too long for
 // loops that have to see a barrier at once.
-__device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, long long limit) {
   if (mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
   while (!mbar_try_wait(bar, parity))
-    if (clock64() - t0 > kTWaitClocks) return false;
+    if (clock64() - t0 > limit) return false;
   return true;
-}
-// The outcome is the same for every lane, so the warp stays converged.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, wait_on(bar, parity));
 }
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
@@ -231,6 +226,10 @@ __global__ void __launch_bounds__(TileShared<TP, D, kAlt>::kThreads, 1) k_attn_t
   volatile int* sodd = reinterpret_cast<volatile int*>(sm + S::oOdd);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto bar = [&](int i) { return base + S::oBars + 8 * i; };
+  // the outcome is the same for every lane, so the warp stays converged
+  auto warp_wait = [&](uint32_t b, uint32_t parity) -> bool {
+    return __all_sync(0xffffffffu, wait_on(b, parity, a.wait_clocks));
+  };
   // Q full / empty; K and V full / empty per stage; per query tile (or, kAlt,
   // S/P buffer): S there, P's upper and lower half there, P V done
   const uint32_t QF = bar(0), QE = bar(1);
@@ -384,6 +383,9 @@ __global__ void __launch_bounds__(TileShared<TP, D, kAlt>::kThreads, 1) k_attn_t
       __syncwarp();
       if (lane == 0) mbar_arrive(b);
     };
+    auto hand_over_q = [&]() {
+      if (!(a.withhold && units == 0 && pw == 0)) arrive(QF);
+    };
     auto load_q = [&](const Unit& x) {
       // the unit's query rows, zeros behind the last
       constexpr int kPer = 32 / kPieces;  // rows a warp copies at once
@@ -458,7 +460,7 @@ __global__ void __launch_bounds__(TileShared<TP, D, kAlt>::kThreads, 1) k_attn_t
             if (!ok) break;
             load_q(x);
             copy_wait<0>();
-            arrive(QF);
+            hand_over_q();
             arrive(KF(s));
           } else {
             copy_wait<1>();
@@ -609,7 +611,7 @@ __global__ void __launch_bounds__(TileShared<TP, D, kAlt>::kThreads, 1) k_attn_t
             if (!ok) break;
             load_q(x);
             copy_wait<0>();
-            arrive(QF);
+            hand_over_q();
           }
           if (v) {
             ++tc_;

@@ -1,6 +1,8 @@
 """What the paged-cache entry points refuse at the edges of their ranges, on the host (no GPU
 needed: only calls that fail validation are made)."""
 
+import ctypes
+
 import pytest
 import torch
 
@@ -33,3 +35,15 @@ def test_more_rows_than_the_kernel_counts_are_refused(name, listed):
         assert _call(fn, _cache(), _rows(n=top, m=m, rows=listed)) == dk.ERR_ARG
     if not torch.cuda.is_available():
         assert _call(fn, _cache(), _rows(n=top, m=0x7FFF0000, rows=listed)) == dk.ERR_UNSUPPORTED
+
+
+def test_the_timeout_self_test_refuses_bad_arguments():
+    fn, c, a = dk.lib().dropkv_selftest_cache_attention_timeout, _cache(), _attn(T=40)
+
+    def call(attn=a, status=FAKE, limit=1000, nbytes=1 << 40):
+        return fn(ctypes.byref(c), ctypes.byref(attn), FAKE, nbytes, status, limit, None)
+
+    assert call(status=None) == call(limit=0) == call(limit=10 ** 9 + 1) == dk.ERR_ARG
+    assert call(status=FAKE + 2) == call(_attn(T=40, q=None)) == dk.ERR_ARG
+    assert call(_attn(T=8)) == call(_attn(T=40, path=dk.PATH_SIMT)) == dk.ERR_UNSUPPORTED
+    assert call(nbytes=16) == dk.ERR_WORKSPACE
