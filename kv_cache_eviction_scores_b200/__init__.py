@@ -49,7 +49,8 @@ __all__ = [
     "DropKVError", "SingularError", "Shape", "Options", "lib", "lib_path",
     "make_shape", "scores_workspace_bytes", "select_workspace_bytes", "dropkv_scores",
     "dropkv_select", "evict", "evict_to_cache", "dropkv_cache_write", "dropkv_cache_read",
-    "dropkv_cache_attention", "cache_attention_workspace_bytes", "cache_attention_path",
+    "dropkv_cache_attention", "cache_attention_workspace", "cache_attention_workspace_bytes",
+    "cache_attention_path",
     "Cache", "CacheRows", "CacheAttn", "auto_path", "scores_launches", "select_launches",
     "selftest_wait_timeout", "selftest_select_timeout", "selftest_cache_attention_timeout",
     "OK", "ERR_ARG", "ERR_SINGULAR", "ERR_CUDA", "ERR_UNSUPPORTED", "ERR_WORKSPACE", "ERR_TIMEOUT",
@@ -685,6 +686,25 @@ def cache_attention_workspace_bytes(cache: Cache, attn: CacheAttn) -> int:
                                                             ctypes.byref(attn)))
 
 
+def cache_attention_workspace(q: torch.Tensor, k_pages: torch.Tensor, page_table: torch.Tensor, *,
+                              path: str = "auto") -> torch.Tensor:
+    """A workspace for dropkv_cache_attention calls of q's and the pages' shapes and
+    dtypes (lengths and values do not matter), on the pages' device: what a captured
+    graph, or a loop of calls on one stream, passes as ``workspace=``."""
+    (B, Hq, T, d), (n_pages, Hkv, page_size, page_d) = q.shape, k_pages.shape
+    if k_pages.dtype not in _PAGE_DTYPES or q.dtype not in _DENSE_DTYPES:
+        raise TypeError("q must be bfloat16 or float32, pages those or float8_e4m3fn")
+    if d != page_d or B != page_table.shape[0]:
+        raise ValueError("q must be [B, Hq, T, d] with the pages' B and d")
+    c = _CACHE_BYTES(B, Hkv, d, n_pages, page_size, page_table.shape[1],
+                     _PAGE_DTYPES[k_pages.dtype], 0, 0, 0, 0, 0, 0)
+    a = _ATTN_BYTES(0, 0, 0, *[0] * 6, _DENSE_DTYPES[q.dtype], Hq, T, 1, 0.0, _PATHS[path], 0, 0)
+    need = _packed_calls()[3](c, a)
+    if need == 0:
+        raise DropKVError(ERR_ARG, "dropkv_cache_attention_workspace_bytes")
+    return torch.empty(need, dtype=torch.uint8, device=k_pages.device)
+
+
 def cache_attention_path(cache: Cache, attn: CacheAttn) -> int:
     return int(lib().dropkv_cache_attention_path(ctypes.byref(cache), ctypes.byref(attn)))
 
@@ -711,7 +731,9 @@ def dropkv_cache_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torc
     A row that sees nothing gives 0 and a log-sum-exp of -inf.  ``scale``:
     default 1/sqrt(d).  ``lse``: fp32 [B, Hq, T], natural logarithm; returned
     with ``return_lse`` or when given.  ``path``: "auto", "simt" (fp32 CUDA
-    cores) or "tensor".  The other arguments are dropkv_cache_write's.
+    cores) or "tensor".  ``workspace``: a tensor of cache_attention_workspace's
+    (one that is too small, or None, is replaced by an allocation); calls that
+    overlap need one each.  The other arguments are dropkv_cache_write's.
     """
     # in fp32, where a small one would become the library's 0 for the default
     if scale is not None and not 0.0 < ctypes.c_float(scale).value < float("inf"):

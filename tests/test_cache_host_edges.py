@@ -47,3 +47,22 @@ def test_the_timeout_self_test_refuses_bad_arguments():
     assert call(status=FAKE + 2) == call(_attn(T=40, q=None)) == dk.ERR_ARG
     assert call(_attn(T=8)) == call(_attn(T=40, path=dk.PATH_SIMT)) == dk.ERR_UNSUPPORTED
     assert call(nbytes=16) == dk.ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("T", [1, 4, 40, 200])
+@pytest.mark.parametrize("dtype,code", [(torch.bfloat16, dk.BF16), (torch.float8_e4m3fn, dk.E4M3)])
+@pytest.mark.parametrize("path", ["auto", "simt", "tensor"])
+def test_a_workspace_from_the_calls_own_tensors(T, dtype, code, path):
+    q = torch.zeros(2, 8, T, 128, dtype=torch.bfloat16)
+    pages = torch.zeros(64, 4, 16, 128).to(dtype)
+    table = torch.zeros(2, 8, dtype=torch.int32)
+    ws = dk.cache_attention_workspace(q, pages, table, path=path)
+    assert ws.dtype == torch.uint8 and ws.numel() == dk.cache_attention_workspace_bytes(
+        _cache(dtype=code), _attn(T=T, path=dk._PATHS[path]))
+    for bad in (q[..., :64], q[:1]):
+        with pytest.raises(ValueError):
+            dk.cache_attention_workspace(bad, pages, table)
+    with pytest.raises(TypeError):
+        dk.cache_attention_workspace(q.half(), pages, table)
+    with pytest.raises(dk.DropKVError):
+        dk.cache_attention_workspace(q[:, :7], pages, table)

@@ -43,3 +43,46 @@ def test_evict_to_cache_refuses_before_any_work(monkeypatch):
                dict(q=q.cpu()), dict(k=k.cpu(), v=k.cpu())):
         with pytest.raises(TypeError):
             call(**kw)
+
+
+def problem(T, fmt, qt=BF16, B=2, Hq=8, Hkv=2, d=128, L=200, seed=1):
+    """Pages with room for 40 slots more, and a chunk of T tokens."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    page, per = 16, -(-(L + 40) // 16)
+    shape = (B * per, Hkv, page, d)
+    s = {x: (torch.randn(shape, generator=g, device=DEV) * (48 if fmt == E4M3 else 1)).to(fmt) for x in "kv"}
+    s["sc"] = dict.fromkeys(("k_scale", "v_scale"))
+    if fmt == E4M3:
+        s["sc"] = {x: torch.randint(119, 124, shape[:3], generator=g, device=DEV, dtype=torch.uint8)
+                   for x in s["sc"]}
+    s["table"] = torch.randperm(B * per, generator=g, device=DEV).to(torch.int32).view(B, per)
+    s["lens"] = i32([L - 13 * b for b in range(B)])
+    s["q"], s["kn"], s["vn"] = (torch.randn(B, H, T, d, generator=g, device=DEV).to(qt)
+                                for H in (Hq, Hkv, Hkv))
+    return s
+
+
+def attend(s, **kw):
+    return dk.dropkv_cache_attention(s["q"], s["k"], s["v"], s["table"], s["lens"], **s["sc"], **kw)
+
+
+CASES = [(1, BF16, BF16), (1, E4M3, BF16), (4, BF16, BF16), (4, E4M3, BF16), (20, BF16, BF16),
+         (20, E4M3, BF16), (100, BF16, BF16), (100, E4M3, BF16), (3, F32, F32), (60, F32, F32)]
+
+
+@pytest.mark.parametrize("T,fmt,qt", CASES)
+def test_a_captured_call_with_a_workspace_of_its_size(T, fmt, qt):
+    s = problem(T, fmt, qt)
+    want = attend(s)
+    out, ws = torch.zeros_like(want), dk.cache_attention_workspace(s["q"], s["k"], s["table"])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        used = torch.cuda.memory_allocated()
+        attend(s, out=out, workspace=ws)
+        assert torch.cuda.memory_allocated() == used
+    for _ in range(2):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
