@@ -264,10 +264,13 @@ __device__ __forceinline__ AttnRow attn_row(const AttnDev& a, int b, int h, int 
   x.hq = h * a.G + (r - x.t * a.G);
   return x;
 }
+// m ln 2 + log l, with ln 2 as two fp32 values: one rounding behind logf's, where the
+// approximate log2 and a product of the sum left three.
 __device__ __forceinline__ void attn_put_lse(const AttnDev& a, const AttnRow& x, float m, float l) {
+  constexpr float kLn2 = 0.69314718055994531, kLn2Rest = 0.69314718055994531 - kLn2;
   if (a.lse)
     a.lse[((int64_t)x.b * a.Hq + x.hq) * a.T + x.t] =
-        l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : (l == 0.f ? -CUDART_INF_F : l);
+        l > 0.f ? fmaf(m, kLn2, fmaf(m, kLn2Rest, logf(l))) : (l == 0.f ? -CUDART_INF_F : l);
 }
 
 // The page and the offset in it of slot `slot` < end of the sequence with this

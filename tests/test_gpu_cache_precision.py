@@ -141,3 +141,43 @@ def test_small_scales_of_v_keep_their_precision(G, T, path):
             tol = tol + A * (2.0 ** -15 + 2.0 ** -20) + 448 * L * 2.0 ** -134
         err = (out[b, :, :c].double().view(2, G, c, 128) - o).abs()
         assert bool((err <= tol).all()), float((err / tol).max())
+
+
+@pytest.mark.parametrize("qt,T", [(BF16, 1), (BF16, 9), (BF16, 20), (BF16, 129), (F32, 1), (F32, 129)])
+def test_the_logarithm_of_exact_sums(qt, T):
+    # logits of 0: a row over L slots sums L weights of 1 exactly, so its lse is logf(L), off by one
+    # unit in the last place at most
+    most, B = 2048, 2048 if T == 1 else 300
+    L = torch.arange(1, B + 1) if B == most else torch.unique((most ** (torch.arange(B) / (B - 1.0))).round().int())
+    B = len(L)
+    k = torch.zeros(most // 64, 1, 64, 64, dtype=qt, device=DEV)
+    table = torch.arange(most // 64, dtype=torch.int32, device=DEV).repeat(B, 1)
+    q = torch.zeros(B, 1, T, 64, dtype=qt, device=DEV)
+    _, lse = dk.dropkv_cache_attention(q, k, k, table, i32(L.tolist()), causal=False, return_lse=True,
+                                       sync=True)
+    want = L.double().log().to(DEV)[:, None, None]
+    err = (lse.double() - want).abs()
+    assert bool((err <= torch.exp2(torch.floor(torch.log2(want.clamp(min=1e-30))) - 23)).all()), float(err.max())
+
+
+@pytest.mark.parametrize("qt,T", [(BF16, 1), (BF16, 64), (F32, 1), (F32, 129)])
+def test_lse_is_as_close_as_the_plain_form(qt, T):
+    # The plain form in fp32 (maximum, exponentials, sum, log) rounds a logit's sum and scaling, the
+    # logarithm and the last sum; this one's roundings are as many.  The two kinds of errors are
+    # independent and differ in size from draw to draw, so the norm over 512 sequences is compared
+    # with room for a fifth.
+    g = torch.Generator(device=DEV).manual_seed(1)
+    B, n = 512, 25
+    L = (torch.arange(B) * 3 + 1).int().to(DEV)
+    k = torch.randn(n, 1, 64, 64, generator=g, device=DEV).to(qt)
+    table = torch.arange(n, dtype=torch.int32, device=DEV).repeat(B, 1)
+    q = torch.randn(B, 1, T, 64, generator=g, device=DEV).to(qt)
+    _, lse = dk.dropkv_cache_attention(q, k, k, table, L, causal=False, return_lse=True, sync=True)
+    K = k.reshape(-1, 64)
+    hidden = torch.arange(len(K), device=DEV)[None, None] >= L[:, None, None]
+    exact = (q[:, 0].double() @ K.double().T / 8).masked_fill(hidden, -math.inf).logsumexp(-1)
+    y = (q[:, 0].float() @ K.float().T * 0.125).masked_fill(hidden, -math.inf)
+    top = y.amax(-1, keepdim=True)
+    plain = top[..., 0] + torch.log(torch.exp(y - top).sum(-1))
+    ours, theirs = ((x.double() - exact).norm() for x in (lse[:, 0], plain))
+    assert float(ours) <= 1.2 * float(theirs), (float(ours), float(theirs))
