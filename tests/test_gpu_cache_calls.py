@@ -78,9 +78,9 @@ def test_a_captured_call_with_a_workspace_of_its_size(T, fmt, qt):
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        used = torch.cuda.memory_allocated()
+        made = torch.cuda.memory_stats()["allocation.all.allocated"]
         attend(s, out=out, workspace=ws)
-        assert torch.cuda.memory_allocated() == used
+        assert torch.cuda.memory_stats()["allocation.all.allocated"] == made
     for _ in range(2):
         out.zero_()
         graph.replay()

@@ -27,7 +27,7 @@ def test_the_cache_calls_allocate_nothing(T, fmt, qt):
 
     step()  # the modules are loaded
     torch.cuda.synchronize()
-    held = torch.cuda.memory_allocated()
+    made = torch.cuda.memory_stats()["allocation.all.allocated"]
 
     def stable():
         free = torch.cuda.mem_get_info()[0]
@@ -37,4 +37,4 @@ def test_the_cache_calls_allocate_nothing(T, fmt, qt):
         return torch.cuda.mem_get_info()[0] == free
 
     assert any(stable() for _ in range(3))  # the device may have other users for a moment
-    assert torch.cuda.memory_allocated() == held
+    assert torch.cuda.memory_stats()["allocation.all.allocated"] == made
