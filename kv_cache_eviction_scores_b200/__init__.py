@@ -745,7 +745,7 @@ def dropkv_cache_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torc
     shape = q.shape
     B, Hq, T, d = shape
     _, Hkv, _, page_d = k_pages.shape
-    if B != page_table.shape[0] or d != page_d or Hq % Hkv:
+    if B != page_table.shape[0] or d != page_d or Hkv < 1 or Hq % Hkv:
         raise ValueError("q must be [B, Hq, T, d] with the pages' B and d and Hq a multiple of Hkv")
     qs = _dense(q, "q", dev, shape)
     if out is None:

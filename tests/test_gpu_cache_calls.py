@@ -86,3 +86,9 @@ def test_a_captured_call_with_a_workspace_of_its_size(T, fmt, qt):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+def test_pages_without_heads_are_refused():
+    z, q = torch.zeros(2, 0, 4, 16, device=DEV), torch.zeros(1, 4, 1, 16, device=DEV)
+    with pytest.raises(ValueError):
+        dk.dropkv_cache_attention(q, z, z, i32([[0, 1]]), i32([3]))
