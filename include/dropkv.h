@@ -284,7 +284,8 @@ DROPKV_API dropkv_status dropkv_scores_select(const dropkv_shape* shape, const v
  * max |x| <= 448 * 2^e (a row of zeros: byte 0).  A power of two costs an 8-bit
  * float no precision, makes scaling exact in both directions, and makes the
  * stored bits independent of the arithmetic.  A row that holds an infinity or a
- * NaN is stored as byte 255 and reads back as NaN.  (Pages that something else
+ * NaN is stored as byte 255 and reads back as NaN.  Finite values from 248 * 2^120
+ * (3.3e38) on round to 2^128 and read back as infinities.  (Pages that something else
  * filled: attention takes a NaN from a row's scale byte only; a value's own NaN
  * code beside a finite scale, which a write never leaves, may count as 480.)
  */
@@ -324,7 +325,8 @@ typedef struct dropkv_cache_rows {
 
 /* Slot start[b] + i of every head of sequence b receives dense row i (row
  * rows[b][h][i] with a list), for i < counts[b].  Other slots stay as they are.
- * Two rows for one slot (pages that occur twice) leave either of them. */
+ * Two rows of one call for one slot (a page that occurs twice in the table) leave
+ * a mixture of them there. */
 DROPKV_API dropkv_status dropkv_cache_write(const dropkv_cache* cache,
                                             const dropkv_cache_rows* rows, int32_t* status_dev,
                                             void* stream);
@@ -345,7 +347,10 @@ DROPKV_API dropkv_status dropkv_cache_read(const dropkv_cache* cache,
  * has no influence on it, whatever it holds (NaN included).  Rows t >= n of out
  * and lse stay as they are.  Query head hq uses KV head hq / (Hq / Hkv).
  * Arithmetic: fp32; on the TENSOR path q, k and v enter as bf16 and the weights
- * that meet v as two bf16 parts (2^-15 of a weight off at most).  *status_dev receives DROPKV_ERR_TIMEOUT if a
+ * that meet v as two bf16 parts (2^-15 of a weight off at most).  Weights are
+ * summed, and multiplied with v, before they are normalised, and each is 2^8 at
+ * most: v whose magnitudes sum to 2^120 or more over the slots may overflow.  Where
+ * v is infinite, a weight under 2^-113 of the row's largest gives NaN.  *status_dev receives DROPKV_ERR_TIMEOUT if a
  * wait inside a kernel gave up (its rows are then undefined). */
 typedef struct dropkv_cache_attn {
   const void* q;        /* device [B, Hq, T, d], strided (last index contiguous)    */
