@@ -19,10 +19,9 @@ struct E4M3 {  // storage only
 // s = ceil(log2 d) and mul = floor(2^32 (2^s - d) / d) + 1, the quotient is
 // (floor(mul n / 2^32) + n) >> s (the sum stays below 2^32).
 struct FastDiv {
-  uint32_t mul, shift, d;
+  uint32_t mul, shift;
   static FastDiv of(uint32_t d) {
     FastDiv f;
-    f.d = d;
     f.shift = 0;
     while ((1ull << f.shift) < d) ++f.shift;
     f.mul = (uint32_t)(((1ull << 32) * ((1ull << f.shift) - d)) / d + 1);

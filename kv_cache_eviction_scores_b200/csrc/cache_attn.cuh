@@ -295,6 +295,19 @@ __device__ __forceinline__ int pool_row(const AttnDev& a, int h, Look k) {
   return -1;
 }
 
+// 16 bytes global -> shared, asynchronously; zeros instead of the source's bytes
+// (which are not read) when !on.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
+  const int n = on ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 struct AttnGrid {
   int ctas, rows, tile;  // of a unit
 };
