@@ -696,6 +696,8 @@ def cache_attention_workspace(q: torch.Tensor, k_pages: torch.Tensor, page_table
         raise TypeError("q must be bfloat16 or float32, pages those or float8_e4m3fn")
     if d != page_d or B != page_table.shape[0]:
         raise ValueError("q must be [B, Hq, T, d] with the pages' B and d")
+    if T == 0:  # no rows, no work
+        return torch.empty(0, dtype=torch.uint8, device=k_pages.device)
     c = _CACHE_BYTES(B, Hkv, d, n_pages, page_size, page_table.shape[1],
                      _PAGE_DTYPES[k_pages.dtype], 0, 0, 0, 0, 0, 0)
     a = _ATTN_BYTES(0, 0, 0, *[0] * 6, _DENSE_DTYPES[q.dtype], Hq, T, 1, 0.0, _PATHS[path], 0, 0)

@@ -66,3 +66,8 @@ def test_a_workspace_from_the_calls_own_tensors(T, dtype, code, path):
         dk.cache_attention_workspace(q.half(), pages, table)
     with pytest.raises(dk.DropKVError):
         dk.cache_attention_workspace(q[:, :7], pages, table)
+
+
+def test_an_empty_chunk_needs_no_workspace():
+    pages, table = torch.zeros(64, 4, 16, 128), torch.zeros(2, 8, dtype=torch.int32)
+    assert dk.cache_attention_workspace(torch.zeros(2, 8, 0, 128), pages, table).numel() == 0
