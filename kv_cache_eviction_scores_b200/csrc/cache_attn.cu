@@ -63,7 +63,16 @@ int64_t group_rows(const dropkv_cache& c, const dropkv_cache_attn& t) {
 }
 
 // The tensor path's kernel by the rows a KV head can have: eight as columns, or
-// 16 as rows, of warp-level products; or query tiles of 128 rows.
+// 16 as rows, of warp-level products; or query tiles of 128 rows.  Both sides of each
+// border, in us over 8 sequences of 16K slots, 8 heads, d = 128, bf16 / e4m3:
+//   8 rows   few 92 / 62      rows 98 / 83
+//   12       few 167 / 108    rows 98 / 84        one query tile 124 / 141
+//   16                        rows 98 / 85        one 124 / 141
+//   20                        rows 174 / 153      one 124 / 141      two 159 / 175
+//   128                                           one 135 / 148      two 165 / 181
+//   132                                           one 238 / 266      two 207 / 222
+// (64 sequences of 2K alike.  One of 32K, where nothing fills the GPU: 20 rows take 41 /
+// 46 as 16-row blocks and 46 / 48 in a query tile, 64 rows 64 / 82 and 49 / 51.)
 enum class Tensor { kFew, kRows, kTile128, kTile256 };
 Tensor tensor_of(const dropkv_cache& c, const dropkv_cache_attn& t) {
   const int64_t rows = group_rows(c, t);

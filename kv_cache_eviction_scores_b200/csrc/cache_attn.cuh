@@ -39,7 +39,7 @@ struct AttnDev {
 constexpr long long kWaitClocks = 4000000000ll;
 
 // An attention kernel's first step.  It may be launched while its predecessor in
-// the stream ends, and waits for that here; only then may the join be launched,
+// the stream ends (those of the tensor path are), and waits for that here; only then may the join be launched,
 // which reads the lengths before its own wait.
 __device__ __forceinline__ void attn_begin() {
   pdl_wait();

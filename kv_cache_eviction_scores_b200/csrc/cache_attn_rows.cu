@@ -490,9 +490,10 @@ __global__ void __launch_bounds__(kRThreads, 1) k_attn_rows(const AttnDev a) {
 // with 16 dims as rows.  Half the matrix instructions and half the registers of
 // the kernel above, whose row block would be half empty; with e4m3 pages, whose
 // tiles are half the bytes, two CTAs then fit an SM, and their warps hide each
-// other's latencies, which bound that kernel there (64 sequences of 2K to 16K
-// e4m3 slots, 7 rows each: 207 us by 16 rows, 119 by eight; four 128K bf16
-// caches, 4 rows each, 320 and 318, 98 % of the measured copy bandwidth).
+// other's latencies, which bound that kernel there (8 rows over 64 sequences of 2K
+// slots: e4m3 91 us by 16 rows, 66 by eight; bf16 97 and 95).  Four 128K bf16 caches,
+// 4 rows each: 2.15 GB in 324 us, 6.6 TB/s, what reads alone reach (the copy that the
+// other figures are held against, half of it writes, has 6.46).
 template <typename TP, int D>
 struct FewShared {
   static constexpr int kDepth = 3;

@@ -567,7 +567,7 @@ __global__ void __launch_bounds__(128) k_attn_merge(const AttnDev a, int ctas) {
   pdl_wait();
   if (kRows >= 128 && pieces <= 4) {
     // large units are cut into few pieces: four rows at a time, lane 4 k + i with
-    // row k's (m, l) of piece i
+    // row k's (m, l) of piece i (4 x 2048 tokens over e4m3 905 us, 922 by the form below)
     for (int r0 = (blockIdx.y * 4 + warp) * 4; r0 < rows; r0 += gridDim.y * 16) {
       auto from = [&](int k, int i) {
         const int slot = i == 0 ? 2 * c0 + 1 : 2 * (c0 + i);
@@ -683,6 +683,15 @@ __global__ void __launch_bounds__(128) k_attn_merge(const AttnDev a, int ctas) {
   }
 }
 
+// Both kernels are launched after their predecessor's end, unlike the others: with the
+// programmatic launch a call of one token took a third longer for head dims of 65 to
+// 128 (8 sequences of 2500 to 5000 fp32 slots, 8 heads, d = 128 129 us against 96; bf16,
+// d = 80 96 against 65), while the others won a microsecond or two.  The SMs keep their
+// split between shared memory and L1 while a kernel is on them, so fewer of these CTAs
+// fit (with the largest share of shared memory asked for, the loss was gone, at 2 to 3 %
+// of every call for the smaller L1).
+constexpr bool kSimtEarly = false;
+
 template <typename TQ, typename TP>
 cudaError_t launch_simt(const AttnDev& a, cudaStream_t st) {
   auto bytes = [](int d) {
@@ -692,7 +701,7 @@ cudaError_t launch_simt(const AttnDev& a, cudaStream_t st) {
   const auto kern = k_attn_simt<TQ, TP>;
   cudaError_t e = allow_smem<k_attn_simt<TQ, TP>>((int)bytes(256));
   if (e != cudaSuccess) return e;
-  return launch_ex(kern, dim3(kSCtas), dim3(kSThreads), smem, st, true, 1, a);
+  return launch_ex(kern, dim3(kSCtas), dim3(kSThreads), smem, st, kSimtEarly, 1, a);
 }
 
 template <typename TQ, typename TP, int kCols>
@@ -702,8 +711,8 @@ cudaError_t launch_simt_cols(const AttnDev& a, int ctas, cudaStream_t st) {
   };
   cudaError_t e = allow_smem<k_attn_simt_tile<TQ, TP, kCols>>((int)bytes(32 * kCols));
   if (e != cudaSuccess) return e;
-  return launch_ex(k_attn_simt_tile<TQ, TP, kCols>, dim3(ctas), dim3(kSThreads), bytes(a.c.d), st, true,
-                   1, a);
+  return launch_ex(k_attn_simt_tile<TQ, TP, kCols>, dim3(ctas), dim3(kSThreads), bytes(a.c.d), st,
+                   kSimtEarly, 1, a);
 }
 
 template <typename TQ, typename TP>
