@@ -569,12 +569,12 @@ def _written(t, name):
     """A tensor that a call writes: no element may stand for two indices."""
     if t.is_contiguous():
         return
-    reach = 1
+    last = 0  # offset of the last element over the strides so far
     for size, stride in sorted(((n, s) for n, s in zip(t.shape, t.stride()) if n > 1),
                                key=lambda x: x[1]):
-        if stride < reach:
+        if stride <= last:
             raise ValueError(f"{name} must not overlap itself")
-        reach = stride * size
+        last += stride * (size - 1)
 
 
 def _launch(fn, what, args, device, status, sync):

@@ -71,3 +71,16 @@ def test_a_workspace_from_the_calls_own_tensors(T, dtype, code, path):
 def test_an_empty_chunk_needs_no_workspace():
     pages, table = torch.zeros(64, 4, 16, 128), torch.zeros(2, 8, dtype=torch.int32)
     assert dk.cache_attention_workspace(torch.zeros(2, 8, 0, 128), pages, table).numel() == 0
+
+
+def test_rows_that_lie_close_are_no_overlap():
+    # the last row of a head ends where the next head begins, with a gap behind the others
+    pages, table = torch.zeros(4, 2, 16, 8), torch.zeros(1, 4, dtype=torch.int32)
+    for strides in ((88, 44, 9, 1), (0, 44, 9, 1), (1, 8, 16, 1)):
+        out = torch.zeros(100).as_strided((1, 2, 5, 8), strides)
+        with pytest.raises(TypeError, match="no CPU path"):  # past the check of out
+            dk.dropkv_cache_read(pages, pages, table, 5, out=(out, out))
+    for strides in ((88, 43, 9, 1), (88, 44, 7, 1), (88, 0, 9, 1), (88, 4, 9, 1)):
+        out = torch.zeros(100).as_strided((1, 2, 5, 8), strides)
+        with pytest.raises(ValueError, match="overlap"):
+            dk.dropkv_cache_read(pages, pages, table, 5, out=(out, out))
