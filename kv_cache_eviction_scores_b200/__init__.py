@@ -538,6 +538,11 @@ def _cache(k_pages, v_pages, page_table, k_scale, v_scale) -> bytes:
                         v_pages.data_ptr(), ks, vs, table)
 
 
+def _rank(t) -> int:
+    """Dimensions of a tensor, 0 of anything else."""
+    return t.dim() if isinstance(t, torch.Tensor) else 0
+
+
 def _int32_on(t, name, device, shape=None):
     """The address of an int32 tensor on the pages' device; None for None."""
     if t is None:
@@ -567,6 +572,8 @@ def _dense(t, name, device, shape):
 
 def _written(t, name):
     """A tensor that a call writes: no element may stand for two indices."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a CUDA tensor on the pages' device")
     if t.is_contiguous():
         return
     last = 0  # offset of the last element over the strides so far
@@ -609,7 +616,7 @@ def _move(fn, what, dense, pages, n, rows, start, counts, status, sync):
     ks, vs = _dense(k, "k", dev, dense_shape), _dense(v, "v", dev, dense_shape)
     if k.dtype != v.dtype:
         raise TypeError("k and v must share one dtype")
-    m = n if rows is None else rows.shape[-1]
+    m = n if rows is None else rows.shape[-1] if _rank(rows) else 0
     r = (None if rows is None else _int32_on(rows, "rows", dev, (B, Hkv, m)),
          None if start is None else _int32_on(start, "start", dev, (B,)),
          None if counts is None else _int32_on(counts, "counts", dev, (B,)))
@@ -644,6 +651,8 @@ def dropkv_cache_write(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor,
     device-side status lands there (ERR_ARG: some page, slot, row or count was
     out of range; what it named was left out); ``sync=True`` waits and raises.
     """
+    if _rank(k) != 4:
+        raise ValueError("k must be a [B, Hkv, n, d] tensor")
     _move(_packed_calls()[0], "dropkv_cache_write", (k, v),
           (k_pages, v_pages, page_table, k_scale, v_scale), k.shape[2], rows, start, counts,
           status, sync)
@@ -665,9 +674,13 @@ def dropkv_cache_read(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: 
     bf16 or fp32 (default: the pages' own, bf16 for e4m3 pages).  The other
     arguments are dropkv_cache_write's.
     """
-    if rows is not None and rows.shape[-1] != n:
-        raise ValueError("rows must list n slots per (sequence, head)")
+    if rows is not None and (_rank(rows) != 3 or rows.shape[-1] != n):
+        raise ValueError("rows must be an int32 tensor that lists n slots per (sequence, head)")
+    if n < 0:
+        raise ValueError("n must not be negative")
     if out is None:
+        if _rank(k_pages) != 4 or _rank(page_table) != 2:
+            raise ValueError("pages must be [n_pages, Hkv, page_size, d] tensors, page_table [B, max_pages]")
         dtype = dtype or (k_pages.dtype if k_pages.dtype in _DENSE_DTYPES else torch.bfloat16)
         shape = (page_table.shape[0], k_pages.shape[1], n, k_pages.shape[3])
         out = tuple(torch.zeros(shape, dtype=dtype, device=k_pages.device) for _ in range(2))

@@ -84,3 +84,23 @@ def test_rows_that_lie_close_are_no_overlap():
         out = torch.zeros(100).as_strided((1, 2, 5, 8), strides)
         with pytest.raises(ValueError, match="overlap"):
             dk.dropkv_cache_read(pages, pages, table, 5, out=(out, out))
+
+
+def test_what_is_no_tensor_or_has_another_rank_is_refused_by_name():
+    pages, table = torch.zeros(4, 2, 16, 8), torch.zeros(1, 4, dtype=torch.int32)
+    x = torch.zeros(1, 2, 5, 8)
+    for k in (None, x[0], x[0, 0], [1.0]):
+        with pytest.raises(ValueError, match="k must"):
+            dk.dropkv_cache_write(k, x, pages, pages, table)
+    for rows in ([1], torch.tensor(5), torch.zeros(5, dtype=torch.int32)):
+        with pytest.raises(ValueError, match="rows must"):
+            dk.dropkv_cache_read(pages, pages, table, 5, rows=rows)
+    for p, t in ((None, table), (pages[0], table), (pages, None), (pages, table[0])):
+        with pytest.raises(ValueError, match="pages must"):
+            dk.dropkv_cache_read(p, pages, t, 5)
+    with pytest.raises(ValueError, match="negative"):
+        dk.dropkv_cache_read(pages, pages, table, -1)
+    with pytest.raises(TypeError, match="out k"):
+        dk.dropkv_cache_read(pages, pages, table, 5, out=(None, None))
+    with pytest.raises(TypeError, match="out v must"):
+        dk.dropkv_cache_read(pages, pages, table, 5, out=(x, [x]))
