@@ -350,8 +350,9 @@ DROPKV_API dropkv_status dropkv_cache_read(const dropkv_cache* cache,
  * that meet v as two bf16 parts (2^-15 of a weight off at most).  Weights are
  * summed, and multiplied with v, before they are normalised, and each is 2^8 at
  * most: v whose magnitudes sum to 2^120 or more over the slots may overflow.  Where
- * v is infinite, a weight under 2^-113 of the row's largest gives NaN.  *status_dev receives DROPKV_ERR_TIMEOUT if a
- * wait inside a kernel gave up (its rows are then undefined). */
+ * v is infinite, a weight under 2^-113 of the row's largest may give NaN.
+ * *status_dev receives DROPKV_ERR_TIMEOUT if a wait inside a kernel gave up (its rows
+ * are then undefined). */
 typedef struct dropkv_cache_attn {
   const void* q;        /* device [B, Hq, T, d], strided (last index contiguous)    */
   void* out;            /* device [B, Hq, T, d], strided                            */
@@ -365,7 +366,8 @@ typedef struct dropkv_cache_attn {
   float scale;          /* > 0, up to FLT_MAX / log2(e); or 0 for 1/sqrt(d)         */
   int32_t path;         /* dropkv_path: AUTO, SIMT (fp32 CUDA cores, any shape) or
                            TENSOR (bf16 q; bf16 or E4M3 pages; d 64 or 128; q, out
-                           and their strides multiples of 16 bytes)                 */
+                           and their strides multiples of 16 bytes; pools of less
+                           than 2^31 rows)                                          */
   const int32_t* lengths;   /* device int32 [B], 0..max_pages * page_size           */
   const int32_t* q_lengths; /* device int32 [B], 0..T, or NULL for T                */
 } dropkv_cache_attn;

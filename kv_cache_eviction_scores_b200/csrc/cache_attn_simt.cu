@@ -9,8 +9,9 @@
 // and reduced by shuffles, and its lanes hold the four rows' O, a column in
 // each 32.  The rows' stride is an odd number of 16-byte pieces, so that the
 // lanes' float4 reads of 32 rows touch every bank evenly.  Bound by latency at
-// small sizes (37 tokens, 6 / 2 heads over two caches of 1501 fp32 slots: 28 us,
-// then the join) and by shared-memory reads at large ones.
+// small sizes (37 tokens, 6 / 2 heads over two caches of up to 1501 fp32 slots: 28 us,
+// then the join; 0.44 instructions a cycle, the stalls on global memory, on shared
+// memory and on dependent results about equal) and by shared-memory reads at large ones.
 #include "cache_attn.cuh"
 #include "tc_ptx.cuh"
 
@@ -684,9 +685,10 @@ __global__ void __launch_bounds__(128) k_attn_merge(const AttnDev a, int ctas) {
 }
 
 // Both kernels are launched after their predecessor's end, unlike the others: with the
-// programmatic launch a call of one token took a third longer for head dims of 65 to
-// 128 (8 sequences of 2500 to 5000 fp32 slots, 8 heads, d = 128 129 us against 96; bf16,
-// d = 80 96 against 65), while the others won a microsecond or two.  The SMs keep their
+// programmatic launch a call of one token took up to 1.7 times as long for head dims of
+// 65 to 128 (8 sequences of 2500 to 5000 slots, 8 heads: fp32, d = 128 137 us against 95;
+// bf16, d = 80 96 against 64, and 371 against 223 for 16K slots), while the others won a
+// microsecond or two.  The SMs keep their
 // split between shared memory and L1 while a kernel is on them, so fewer of these CTAs
 // fit (with the largest share of shared memory asked for, the loss was gone, at 2 to 3 %
 // of every call for the smaller L1).
@@ -726,9 +728,11 @@ cudaError_t launch_simt_tile(const AttnDev& a, int ctas, cudaStream_t st) {
 }  // namespace
 
 // Tiles of 64 rows where they are filled twice; below that, pieces of 16, which
-// read K and V again but leave more CTAs at work.  Both measured (fp32, d = 64):
-// 111 rows of 8 heads' worth over 1501 slots 33 and 47 us, 70 x 8 heads over 4000
-// 68 and 73, 420 x 8 over 3000 184 and 117, 1200 x 2 over 1000 53 and 55.
+// read K and V again but leave more CTAs at work.  Both measured (fp32 slots, d = 64, us
+// by 16 and by 64 rows): two sequences of 1501 with 111 rows x 2 heads 35 and 43, one of
+// 4000 with 70 x 4 41 and 61, with 72 x 8 66 and 68, one of 3000 with 420 x 8 199 and
+// 125, one of 1000 with 1200 x 2 58 and 59; 300 x 8 over 3000 with d = 128 232 and 158,
+// with d = 256 490 and 517.
 AttnGrid attn_grid_simt(int64_t rows, int d) {
   if (rows <= 128) return {kSCtas, kSRows, kSTile};
   return {d <= 64 ? kLCtas3 : kLCtas, kLRows, kSTile};

@@ -10,9 +10,12 @@
 // 16-byte loads and stores; the row's maximum by shuffles inside the group) and
 // moves K and V of that row together; kRowsInFlight rows per group keep their
 // loads in flight, as they are stored; the list, page table and slot arithmetic
-// are done once per row, by one thread.  Measured: 0.74 GB of bf16 rows to e4m3
-// in 141 us (5.3 TB/s, 81 % of the measured copy; 188 us with four rows placed by
-// every lane and fp32 arithmetic), 0.2 GB of e4m3 back to bf16 in 37 us (5.4).
+// are done once per row, by one thread.  Measured (one call after the other): 0.74 GB
+// of bf16 rows to e4m3 in 141 us (5.3 TB/s, 81 % of the measured copy; 188 us with four
+// rows placed by every lane and fp32 arithmetic; 143 to 150 as calls over changing
+// inputs), 0.2 GB of e4m3 back to bf16 in 37 us (5.4; 38).  Rows that 16-byte pieces do
+// not fit (d = 33) move value by value, one row in flight: 32K x 8 bf16 rows 100 us,
+// their bytes 11.
 #include "cache.cuh"
 
 namespace dropkv {
