@@ -347,7 +347,9 @@ DROPKV_API dropkv_status dropkv_cache_read(const dropkv_cache* cache,
  * has no influence on it, whatever it holds (NaN included).  Rows t >= n of out
  * and lse stay as they are.  Query head hq uses KV head hq / (Hq / Hkv).
  * Arithmetic: fp32; on the TENSOR path q, k and v enter as bf16 and the weights
- * that meet v as two bf16 parts (2^-15 of a weight off at most).  Weights are
+ * that meet v as two bf16 parts (2^-15 of a weight off at most); its matrix products
+ * cut their sums off, so that v of one sign comes out too small by up to some 1.2e-4
+ * (at 128K slots; with up to 16 rows a KV head in proportion above that).  Weights are
  * summed, and multiplied with v, before they are normalised, and each is 2^8 at
  * most: v whose magnitudes sum to 2^120 or more over the slots may overflow.  Where
  * v is infinite, a weight under 2^-113 of the row's largest may give NaN.

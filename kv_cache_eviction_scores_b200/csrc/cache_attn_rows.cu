@@ -8,7 +8,9 @@
 // here), so O is rarely rescaled.  l sums the fp32 P; the P that meets V is
 // taken as two bf16 parts (lower_bf16x2).  e4m3 pages: a value is widened exactly
 // to bf16, K's row scale multiplies the logit and V's multiplies P before it is
-// split (a power of two: exact), so nothing else is rounded.
+// split (a power of two: exact), so nothing else is rounded.  (The products cut O's sums
+// off, about 2^-24 of them a time: V of one sign comes out 1.2e-4 too small over 128K
+// slots that one CTA sums, n / 64 products a warp.)
 //
 // What bounds it: reading the pages.  Layout: a unit of 16 rows is one
 // m16n8k16 row block, so each K/V byte is used for 16 rows' products by the

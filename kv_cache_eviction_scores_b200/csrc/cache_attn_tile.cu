@@ -47,7 +47,14 @@ using namespace tc;
 constexpr int kTTile = 128, kTCtas = 148;
 constexpr int kTMmaWarp = 12;  // the softmax warps, the producers, then the MMA issuers
 constexpr uint32_t kTColO = 256;
-
+// The tensor core cuts its sums off, by 1.7 x 2^-24 of them on average at each of a slot
+// tile's 16 P V steps: always downwards, so that O over 128K slots of V of one sign came
+// out 1.6e-3 too small (half a step of bf16 is 2e-3 to 3.9e-3).  So every kFold slot
+// tiles the softmax threads add O to their rows in the workspace, rounding to nearest,
+// and P V begins from 0: 1.2e-4 then, for 0 to 3 % of the time (256 tokens x 8 over 64K
+// bf16 slots 777 us, 748 to 781 without; 16 tokens x 8 over 128K e4m3 slots 963 and 967).
+// Every 64 tiles: 8e-5, and 4 to 7 % (807 us).
+constexpr int kFold = 128;
 
 template <typename TP, int D, bool kAlt>
 struct TileShared {
@@ -161,6 +168,30 @@ __device__ __forceinline__ Unit unit_of(const AttnDev& a, const AttnWalk& w) {
   x.seen_all = attn_seen(a, x.L, x.n, x.rt * kRows + x.rows - 1);
   x.seen_min = attn_seen(a, x.L, x.n, x.rt * kRows);
   return x;
+}
+
+__device__ __forceinline__ void prefetch_l2(const float* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+// o += 2^(mp - m) from, and to = o, over 32 columns.
+__device__ __forceinline__ void add_part(uint32_t (&o)[32], const float* from, float mp, float m, bool on) {
+  if (!on) return;
+  const float f = mp == -CUDART_INF_F ? 0.f : attn_ex2(mp - m);
+  float4 z[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) z[k] = reinterpret_cast<const float4*>(from)[k];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    o[4 * k] = u32(fmaf(z[k].x, f, f32(o[4 * k])));
+    o[4 * k + 1] = u32(fmaf(z[k].y, f, f32(o[4 * k + 1])));
+    o[4 * k + 2] = u32(fmaf(z[k].z, f, f32(o[4 * k + 2])));
+    o[4 * k + 3] = u32(fmaf(z[k].w, f, f32(o[4 * k + 3])));
+  }
+}
+__device__ __forceinline__ void put_part(float* to, const uint32_t (&o)[32]) {
+#pragma unroll
+  for (int k = 0; k < 32; k += 4)
+    *reinterpret_cast<float4*>(to + k) = make_float4(f32(o[k]), f32(o[k + 1]), f32(o[k + 2]), f32(o[k + 3]));
 }
 
 // The infinities and NaNs of V that a row sees, of its unit's partly seen
@@ -338,7 +369,7 @@ __global__ void __launch_bounds__(TileShared<TP, D, kAlt>::kThreads, 1) k_attn_t
 #pragma unroll
               for (int kk = 0; kk < 8; ++kk)  // both parts of P for each V slice of 16 rows, 2 KB
                 mma_ts_w(dO, tbase + 128u * f + 64u * half + 8u * kk, vlo + 128u * (4 * half + (kk >> 1)),
-                         vd.hi, IDP, (j > 0 || half == 0 || kk > 0) ? 1u : 0u);
+                         vd.hi, IDP, (j % kFold > 0 || half == 0 || kk > 0) ? 1u : 0u);
             }
           }
           if (!ok) break;
@@ -644,9 +675,40 @@ __global__ void __launch_bounds__(TileShared<TP, D, kAlt>::kThreads, 1) k_attn_t
       const int seen = has ? attn_seen(a, x.L, x.n, r) : 0;
       float m = -CUDART_INF_F, l = 0.f;
       const bool mine = 128 * u < x.rows;  // this query tile exists
+      // Where O goes on the way, and the reference that it has there: the unit's partial,
+      // or for a whole unit that of the CTA's last one, which is written behind it.
+      // Where O goes on the way: the unit's partial, or for a whole unit that of the CTA's
+      // last one, which is written behind it.  mp: the reference that O has there.
+      auto part_row = [&]() {
+        const int slot = attn_slot(w);
+        return a.part + ((size_t)(slot < 0 ? 2 * (int)blockIdx.x + 1 : slot) * kRows + crow) * a.pstride;
+      };
+      float mp = -CUDART_INF_F;
       for (int j = 0; j < T && live && mine; ++j) {
         const int f = kAlt ? n & 1 : u;  // S/P buffer
         const uint32_t tS = tbase + 128u * f + lane_off;
+        if (warp_rows && j > 0 && j % kFold == 0) {
+          // O, complete up to the last tile, to its row in the workspace
+          if (!warp_wait(PD(kAlt ? f ^ 1 : u), (kAlt ? (n - 1) >> 1 : n - 1) & 1)) {
+            alive(false);
+            break;
+          }
+          tc_fence_after();
+#pragma unroll 1
+          for (int k = 0; k < D / 32; ++k) {
+            uint32_t o[32];
+            tmem_ld32(tO + 32u * k, o);
+            if (j > kFold) add_part(o, part_row() + 32 * k, mp, m, has);
+            if (has) put_part(part_row() + 32 * k, o);
+          }
+          mp = m;
+        }
+        if (has && j >= kFold && ((j + 1) % kFold == 0 || j + 1 == T)) {
+          // what the next tile's fold, or the unit's end, reads: behind the copies in
+          // flight its way from memory takes microseconds
+#pragma unroll
+          for (int k = 0; k < D; k += 32) prefetch_l2(part_row() + k);
+        }
         alive(warp_wait(SF(f), (kAlt ? n >> 1 : n) & 1));
         if (!live) break;
         if (warp_rows) {
@@ -749,13 +811,14 @@ __global__ void __launch_bounds__(TileShared<TP, D, kAlt>::kThreads, 1) k_attn_t
         ++n;
       }
       // ---- the unit's rows: O / l, or the cut unit's partial ----
-      const int slot = attn_slot(w);
       const AttnRow at = attn_row(a, x.b, w.h, has ? r : x.rt * kRows);
       __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) + at.b * a.os[0] +
                            at.hq * a.os[1] + at.t * a.os[2];
-      float* part = a.part + ((size_t)(slot < 0 ? 0 : slot) * kRows + crow) * a.pstride;
       const int j0 = max(w.t0 * kTTile, x.seen_min), j1 = min(w.t1 * kTTile, seen);
+      const int slot = attn_slot(w);
+      float* part = part_row();
       auto finish = [&](uint32_t (&o)[32], int c0, bool fix, float inv) {
+        if (T > kFold) add_part(o, part + c0, mp, m, has);
         if (fix) add_non_finite<TP, D>(a, x.b, w.h, j0, j1, c0, o);
         if (!has) return;
         if (slot < 0) {
@@ -768,10 +831,7 @@ __global__ void __launch_bounds__(TileShared<TP, D, kAlt>::kThreads, 1) k_attn_t
             *reinterpret_cast<uint4*>(out + c0 + k) = make_uint4(y[0], y[1], y[2], y[3]);
           }
         } else {
-#pragma unroll
-          for (int k = 0; k < 32; k += 4)
-            *reinterpret_cast<float4*>(part + c0 + k) =
-                make_float4(f32(o[k]), f32(o[k + 1]), f32(o[k + 2]), f32(o[k + 3]));
+          put_part(part + c0, o);
         }
       };
       auto put_stats = [&](float mm, float ll) {

@@ -181,3 +181,87 @@ def test_lse_is_as_close_as_the_plain_form(qt, T):
     plain = top[..., 0] + torch.log(torch.exp(y - top).sum(-1))
     ours, theirs = ((x.double() - exact).norm() for x in (lse[:, 0], plain))
     assert float(ours) <= 1.2 * float(theirs), (float(ours), float(theirs))
+
+
+@pytest.mark.parametrize("pt", [BF16, E4M3])
+@pytest.mark.parametrize("G,T", [(4, 1), (4, 4), (4, 16), (4, 512)])
+def test_outputs_over_a_long_range_that_no_split_shortens(pt, G, T):
+    # V of one sign and weights that are no powers of two, so that nothing is exact and every sum
+    # that a matrix product cuts off errs downwards.  How much an instruction cuts off is documented
+    # nowhere: one unit of the total's last place, 2^-23, where it is cut once, and 2^-22 is allowed.
+    # One instruction takes 16 slots and one of a weight's two parts.  Up to 16 rows, eight warps
+    # share the slots: n / 64 instructions each.  Above, O leaves the tensor core every 128 tiles of
+    # 128 slots: 2048 instructions, and n / 16384 sums of 2^-24.  Besides: a weight's two parts (2^-15
+    # and 2^-20), ex2 and the exponent's rounding (2^-21) in the weight and in l, whose sums are of
+    # 128 + n / 128 terms; the output's own rounding, 2^-8.
+    d, Hkv, L = 128, 8, 131072
+    B = 37 if T < 512 else 3                        # with units to fill the CTAs
+    n = L // 128
+    g = torch.Generator(device=DEV).manual_seed(T)
+    off = 1 + torch.arange(Hkv * d, device=DEV).view(1, Hkv, 1, d) / (Hkv * d)
+    v = off + 0.3 * torch.rand(n, Hkv, 128, d, generator=g, device=DEV)
+    k = torch.zeros(n, Hkv, 128, d, device=DEV)
+    k[1:, :, :, 0] = 1                              # the first 128 slots set the reference
+    k, v = k.to(pt), (v * 64).to(pt)
+    sc = torch.full((n, Hkv, 128), 127, dtype=torch.uint8, device=DEV) if pt == E4M3 else None
+    table = torch.arange(n, dtype=torch.int32, device=DEV).repeat(B, 1)
+    q = torch.zeros(B, Hkv * G, T, d, device=DEV, dtype=BF16)
+    q[..., 0] = 9.625
+    w = torch.full((L,), math.exp(9.625 / math.sqrt(d)), dtype=torch.float64, device=DEV)
+    w[:128] = 1
+    want = torch.einsum("nhsd,ns->hd", v.double(), w.view(n, 128)) / w.sum()
+    out = dk.dropkv_cache_attention(q, k, v, table, i32([L] * B), causal=False, k_scale=sc, v_scale=sc,
+                                    sync=True)
+    chain = L / 64 if G * T <= 16 else 2048 + L / 16384
+    rel = chain * 2.0 ** -22 + 2.0 ** -15 + 2.0 ** -20 + 2 * 2.0 ** -21 + (128 + L / 128) * 2.0 ** -24
+    err = (out.double().view(B, Hkv, G * T, d) / want[None, :, None] - 1).abs().max()
+    assert float(err) <= 2.0 ** -8 + rel, (float(err), rel)
+
+
+@pytest.mark.parametrize("pt", [BF16, E4M3])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G,T", [(4, 30), (4, 80), (3, 43)])
+def test_references_that_move_between_parts_of_a_long_sum(pt, d, G, T):
+    # logits that grow along the slots, ragged and causal, whole units and cut ones (with units to
+    # fill the CTAs, many of them have over 256 tiles to themselves); infinities and a NaN early on
+    B, Hkv, page = 21, 8, 64
+    L = [40000 - 1042 * b for b in range(B)]
+    n = -(-L[0] // page)
+    g = torch.Generator(device=DEV).manual_seed(T + d)
+    k, v = (torch.randn(n, Hkv, page, d, generator=g, device=DEV) for _ in range(2))
+    k *= (0.5 + 1.5 * torch.arange(n, device=DEV) / n)[:, None, None, None]
+    sc = None
+    if pt == E4M3:
+        k, v = k * 32, v * 32
+        sc = torch.full((n, Hkv, page), 122, dtype=torch.uint8, device=DEV)
+    k, v = k.to(pt), v.to(pt)
+    odd = () if pt == E4M3 else (3, 5, 9)
+    if odd:
+        v[10, :, 7, 3], v[90, :, 7, 5], v[2, :, 0, 9] = math.inf, -math.inf, math.nan
+    table = torch.arange(n, dtype=torch.int32, device=DEV).repeat(B, 1)
+    q = torch.randn(B, Hkv * G, T, d, generator=g, device=DEV).to(BF16)
+    out, lse = dk.dropkv_cache_attention(q, k, v, table, i32(L), k_scale=sc, v_scale=sc,
+                                         return_lse=True, sync=True)
+    if odd:
+        assert (out[..., 3] == math.inf).all() and (out[..., 5] == -math.inf).all()
+        assert torch.isnan(out[..., 9]).all()
+    rest = [i for i in range(d) if i not in odd]
+    K, V = (x.double().permute(1, 0, 2, 3).reshape(Hkv, n * page, d) * (1 if sc is None else 2.0 ** -5)
+            for x in (k, v))
+    V = V[..., rest]
+    for b in (0, 1, 10, 20):
+        x, c = q[b].double().view(Hkv, G * T, d), L[b]
+        seen = (torch.arange(c, device=DEV) <= (c - T + torch.arange(T, device=DEV))[:, None]).repeat(G, 1)
+        for h in range(Hkv):
+            y = (x[h] @ K[h, :c].T / math.sqrt(d)).masked_fill(~seen, -math.inf)
+            w = torch.logsumexp(y, -1)
+            p = torch.exp(y - w[:, None])
+            o, A = p @ V[h, :c], p @ V[h, :c].abs()
+            S = (x[h].abs() @ K[h, :c].abs().T / math.sqrt(d)).masked_fill(~seen, 0).amax(-1)
+            Y = y.masked_fill(~seen, 0).abs().amax(-1)
+            tol, ltol = R.bounds(o, w, A, S, Y, d, c, BF16, False)
+            tol = tol + A * (2.0 ** -15 + 2.0 ** -20)
+            err = (out[b].view(Hkv, G * T, d)[h][:, rest].double() - o).abs()
+            assert bool((err <= tol).all()), float((err / tol).max())
+            err = (lse[b].view(Hkv, G * T)[h].double() - w).abs()
+            assert bool((err <= ltol).all()), float((err / ltol).max())
