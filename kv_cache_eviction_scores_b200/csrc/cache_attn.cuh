@@ -10,7 +10,8 @@
 // with one scan over the (b, row tile) items.  A unit that lies within one
 // range is finished there; a unit that is cut leaves one partial per CTA (the
 // unnormalised O, the reference maximum m and the sum l of each row), which
-// k_attn_merge joins in the order of the slots.
+// k_attn_merge joins in the order of the slots.  (The tile kernel keeps parts of a
+// long unit's O there, too, until the unit is finished.)
 #pragma once
 
 #include "cache.cuh"

@@ -675,8 +675,6 @@ __global__ void __launch_bounds__(TileShared<TP, D, kAlt>::kThreads, 1) k_attn_t
       const int seen = has ? attn_seen(a, x.L, x.n, r) : 0;
       float m = -CUDART_INF_F, l = 0.f;
       const bool mine = 128 * u < x.rows;  // this query tile exists
-      // Where O goes on the way, and the reference that it has there: the unit's partial,
-      // or for a whole unit that of the CTA's last one, which is written behind it.
       // Where O goes on the way: the unit's partial, or for a whole unit that of the CTA's
       // last one, which is written behind it.  mp: the reference that O has there.
       auto part_row = [&]() {
@@ -700,6 +698,7 @@ __global__ void __launch_bounds__(TileShared<TP, D, kAlt>::kThreads, 1) k_attn_t
             tmem_ld32(tO + 32u * k, o);
             if (j > kFold) add_part(o, part_row() + 32 * k, mp, m, has);
             if (has) put_part(part_row() + 32 * k, o);
+            __syncwarp();
           }
           mp = m;
         }
